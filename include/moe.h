@@ -34,7 +34,9 @@
  *    ZERO-FILLED before its first use; every call leaves the control block's
  *    counters at zero again, so one workspace can be reused by any sequence
  *    of calls of any shapes on one stream.  Calls that overlap in time must
- *    not share a workspace.
+ *    not share a workspace.  (moe_rms_norm_grad, moe_balance_loss and
+ *    moe_gate_grad neither read nor write the control block: any memory
+ *    serves as their workspace, zero-filled or not.)
  *  - Errors: arguments are validated on the host only (scalars and non-null
  *    pointers); a violation returns MOE_E_INVAL and enqueues nothing.  A
  *    workspace below the required size returns MOE_E_WORKSPACE.  An
@@ -357,6 +359,183 @@ moe_status moe_layer_noalloc(const void* x, const void* gate, int gate_is_fp32, 
  * expected number of 32-row GEMM1 tiles, E (1 - (1 - k/E)^T) * 2F / 256,
  * reaches 400 (bf16) or 320 (MXFP4), else 16. */
 int moe_layer_block_m(int T, int E, int F, int k, int wformat);
+
+/* ------------------------------------------------------------------------
+ * moe_rms_norm - the root-mean-square norm in front of the layer, with the
+ * residual's addition before it and the activation quantisation of the
+ * expert GEMMs behind it:
+ *   h = x + residual,   y = h * rsqrt(mean(h^2) + eps) * weight.
+ *
+ *  x          bf16 [T, H]
+ *  residual   [T, H], float32 if residual_is_fp32 is 1, bf16 if 0; NULL: none
+ *             (h = x)
+ *  weight     [H], float32 if weight_is_fp32 is 1, bf16 if 0
+ *  eps        finite, >= 0
+ *  qformat    the moe_wformat whose activation format q and s take:
+ *             MOE_W_BF16 none; MOE_W_FP8_BLOCK128 (H a multiple of 128)
+ *             q e4m3 [T, H], s float32 [T, H/128], amax / 448 per group (1
+ *             for a group of zeros); MOE_W_MXFP4 (H a multiple of 32) q e4m3
+ *             [T, H], s e8m0 [T, H/32], the smallest power of two of at
+ *             least amax / 448
+ *  h          out, the residual's type; NULL: not wanted.  Needs a residual
+ *  y          out, bf16 [T, H]; may be NULL with a qformat other than BF16
+ *  q, s       out, used with a qformat other than BF16
+ * The sum, the norm and the values that are quantised are fp32, taken from
+ * the unrounded h; y, h and q are each rounded once (q not from the bf16 y).
+ * h may be the residual or x itself, and y may be x; the outputs overlap
+ * nothing else.  A row with a NaN gives NaN in y and q (scales 1); mean(h^2)
+ * is an fp32 value, so a row whose sum of squares passes 3.4e38 gives zeros
+ * (and NaN where h is infinite).
+ * x, residual, weight, h and y need the alignment of an element only, s
+ * too; q 8 bytes.  No workspace.  Constraints: 0 <= T <= 2^24, 1 <= H;
+ * H > 32768, or an H that the format's group does not divide:
+ * MOE_E_UNSUPPORTED.
+ * ------------------------------------------------------------------------ */
+moe_status moe_rms_norm(const void* x, const void* residual, int residual_is_fp32,
+                        const void* weight, int weight_is_fp32, int T, int H,
+                        float eps, int qformat, void* h, void* y, void* q, void* s,
+                        hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_rms_norm_grad - the gradient of moe_rms_norm:
+ *   r = rsqrt(mean(h^2) + eps), g = dy * weight,
+ *   dx = r g - h r^3 mean(g h) + dh,   d_weight = sum over rows of dy h r.
+ *
+ *  dy         bf16 [T, H], the gradient of y (of the values that q stands
+ *             for, where those are used)
+ *  dh         [T, H], the gradient that reaches h from elsewhere, h's type;
+ *             NULL: none
+ *  h          [T, H], the h of the forward call (x where it had no
+ *             residual), float32 if h_is_fp32 is 1, bf16 if 0
+ *  dx         out, [T, H], h's type: the gradient of x and of the residual.
+ *             May be dh or h itself; overlaps nothing else
+ *  d_weight   out, float32 [H]; NULL: not wanted (then no workspace)
+ * Sums in fp32 and in a fixed order: the same result every time.  T = 0
+ * writes a zero d_weight.  Constraints as moe_rms_norm.
+ * ------------------------------------------------------------------------ */
+moe_status moe_rms_norm_grad(const void* dy, const void* dh, const void* h, int h_is_fp32,
+                             const void* weight, int weight_is_fp32, int T, int H,
+                             float eps, void* dx, float* d_weight,
+                             void* workspace, size_t workspace_bytes,
+                             hipStream_t stream);
+size_t moe_rms_norm_grad_workspace_size(int T, int H);
+
+/* ------------------------------------------------------------------------
+ * moe_norm_layer - moe_rms_norm, then moe_layer on its result, on one
+ * stream: y = layer(norm(x + residual)), h = x + residual.  The router (and
+ * bf16 experts) read the bf16 normalised states; for the fp8 formats the
+ * norm also writes the experts' activations, so the layer's own
+ * quantisation, and its rounding to bf16 before it, fall away.
+ *
+ * Arguments as moe_rms_norm (norm_weight: its weight; h may be NULL) and
+ * moe_layer.  The workspace must hold moe_norm_layer_workspace_size bytes.
+ * For MOE_W_BF16 the bits of y equal moe_rms_norm followed by moe_layer.
+ * ------------------------------------------------------------------------ */
+moe_status moe_norm_layer(const void* x, const void* residual, int residual_is_fp32,
+                          const void* norm_weight, int norm_weight_is_fp32, float eps,
+                          const void* gate, int gate_is_fp32, const float* bias,
+                          int wformat, const void* w13, const void* w13_scale,
+                          const void* w2, const void* w2_scale,
+                          int T, int H, int E, int F, int k, int n_shared,
+                          int n_group, int topk_group, int scoring,
+                          int renormalize, float routed_scale, int block_m,
+                          float swiglu_limit, void* h, void* y,
+                          int32_t* topk_ids_out, float* topk_weights_out,
+                          void* workspace, size_t workspace_bytes,
+                          hipStream_t stream);
+size_t moe_norm_layer_workspace_size(int T, int H, int E, int F, int k, int n_shared,
+                                     int block_m, int wformat);
+
+/* ------------------------------------------------------------------------
+ * moe_balance_loss - the router's load-balance loss over sequences, the z
+ * loss, and the per-expert counts.
+ *
+ *  logits       float32 [T, E] (moe_route's logits_out)
+ *  topk_ids     int32 [T, k + n_shared] (moe_route's or moe_route_align's;
+ *               slots from k on are the shared expert's and are passed
+ *               over).  An id outside [0, E) is not counted; an id that a
+ *               row names twice counts twice
+ *  token_mask   uint8 [T]: rows with 0 (padding) take no part; NULL: none
+ *  seq_offsets  int32 [n_seq + 1], ascending within [0, T], on the device:
+ *               sequence s is the rows seq_offsets[s] .. seq_offsets[s+1]-1
+ *               (none, where they are equal); rows before the first and
+ *               behind the last sequence take no part.  NULL: the whole
+ *               batch is one sequence (n_seq = 1).  Values out of order
+ *               give undefined numbers, and no access outside a buffer
+ *  losses       out, float32 [2]:
+ *    [0] = 1/S' sum_s sum_e (E counts[s,e] / (k n_s)) probs[s,e]
+ *    [1] = 1/N sum_t logsumexp(logits[t])^2
+ *    over the n_s tokens of sequence s that take part, the S' sequences
+ *    with n_s > 0 and all N = sum n_s tokens (0 where there are none)
+ *  counts       out, int32 [n_seq, E]
+ *  probs        out, float32 [n_seq, E]: the mean over the sequence's tokens
+ *               of p = score / (sum of the row's scores + 1e-20) (softmax:
+ *               the softmax); 0 where n_s = 0
+ *  tokens       out, int32 [n_seq + 2]: n_s, then N, then S'
+ * A logit of -inf is an expert of score 0; a row of -inf only counts as a
+ * token with p = 0 and no z.  A NaN in a row that takes part reaches the
+ * losses; rows that do not are not read.  Sums are fp32 in a fixed order
+ * (fp64 over sequences).
+ * Constraints: 0 <= T <= 2^24, 1 <= k <= E <= 1024, k + n_shared <= 16,
+ * n_shared in {0, 1}, 1 <= n_seq <= 2^20.
+ * ------------------------------------------------------------------------ */
+moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids,
+                            const uint8_t* token_mask, const int32_t* seq_offsets,
+                            int T, int E, int k, int n_shared, int n_seq, int scoring,
+                            float* losses, int32_t* counts, float* probs,
+                            int32_t* tokens, void* workspace, size_t workspace_bytes,
+                            hipStream_t stream);
+size_t moe_balance_loss_workspace_size(int T, int E, int n_seq);
+
+/* ------------------------------------------------------------------------
+ * moe_route_grad - the gradient to the logits, in one pass, of the routing
+ * weights and of both losses.
+ *
+ *  logits .. n_seq, scoring   as given to moe_balance_loss
+ *  renormalize, routed_scale  as given to moe_route
+ *  d_weights    float32 [T, k + n_shared], the gradient of topk_weights
+ *               (slots from k on are passed over); NULL: none
+ *  d_losses     float32 [2] on the device, the gradient of losses (the
+ *               losses' coefficients); NULL: none.  Not both NULL
+ *  counts, tokens   moe_balance_loss's outputs (used with d_losses).  They
+ *               carry no gradient, as the choice of the experts does not
+ *  d_logits     out, float32 [T, E]
+ * The losses' part covers the rows that take part in them; the weights'
+ * part covers every row (slots whose id lies outside [0, E) have no weight).
+ * A row with neither (no loss, and no d_weights but zeros) is written as
+ * zeros whatever its logits are.  No workspace.  Constraints as
+ * moe_balance_loss.
+ * ------------------------------------------------------------------------ */
+moe_status moe_route_grad(const float* logits, const int32_t* topk_ids,
+                          const uint8_t* token_mask, const int32_t* seq_offsets,
+                          int T, int E, int k, int n_shared, int n_seq, int scoring,
+                          int renormalize, float routed_scale, const float* d_weights,
+                          const float* d_losses, const int32_t* counts,
+                          const int32_t* tokens, float* d_logits, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * moe_gate_grad - from the logits' gradient to the hidden states and the
+ * gate:
+ *   dx = d_logits gate + dx_in,   d_gate = d_logits^T x.
+ *
+ *  x          bf16 [T, H]           (used for d_gate)
+ *  gate       [E, H], float32 if gate_is_fp32 is 1, bf16 if 0 (used for dx)
+ *  d_logits   float32 [T, E]
+ *  dx_in      bf16 [T, H], added before dx is rounded; NULL: none.  Needs dx
+ *  dx         out, bf16 [T, H]; may be dx_in itself; NULL: not wanted
+ *  d_gate     out, float32 [E, H]; NULL: not wanted (not both)
+ * Sums are fp32 in a fixed order.  d_gate's products are exact (the fp32
+ * d_logits as three bf16 parts); dx, rounded to bf16, leaves out parts below
+ * 2^-15 of each product.  T = 0 writes a zero d_gate.  An operand that is
+ * not finite makes the rows it meets not finite (an infinity may become a
+ * NaN).  Constraints: 0 <= T <= 2^24, H a multiple of 128 and at most 2^20,
+ * 1 <= E <= 1024.
+ * ------------------------------------------------------------------------ */
+moe_status moe_gate_grad(const void* x, const void* gate, int gate_is_fp32,
+                         const float* d_logits, const void* dx_in, int T, int H, int E,
+                         void* dx, float* d_gate, void* workspace,
+                         size_t workspace_bytes, hipStream_t stream);
+size_t moe_gate_grad_workspace_size(int T, int H, int E);
 
 /* ------------------------------------------------------------------------
  * Diagnostics and measurement probes (not part of the layer).

@@ -67,6 +67,17 @@ SIGNATURES = {
     "moe_layer_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
     "moe_layer_noalloc": (_i, [_vp, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _i, _i, _f,
                                _i, _f, _vp, _vp, _vp, _vp]),
+    "moe_rms_norm": (_i, [_vp, _vp, _i, _vp, _i, _i, _i, _f, _i, _vp, _vp, _vp, _vp, _vp]),
+    "moe_rms_norm_grad": (_i, [_vp, _vp, _vp, _i, _vp, _i, _i, _i, _f, _vp, _vp, _vp, _sz, _vp]),
+    "moe_rms_norm_grad_workspace_size": (_sz, [_i, _i]),
+    "moe_norm_layer": (_i, [_vp, _vp, _i, _vp, _i, _f, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i,
+                            _i, _i, _i, _i, _f, _i, _f, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_norm_layer_workspace_size": (_sz, [_i, _i, _i, _i, _i, _i, _i, _i]),
+    "moe_balance_loss": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "moe_balance_loss_workspace_size": (_sz, [_i, _i, _i]),
+    "moe_route_grad": (_i, [_vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp, _vp, _vp, _vp, _vp]),
+    "moe_gate_grad": (_i, [_vp, _vp, _i, _vp, _vp, _i, _i, _i, _vp, _vp, _vp, _sz, _vp]),
+    "moe_gate_grad_workspace_size": (_sz, [_i, _i, _i]),
     "moe_layer_block_m": (_i, [_i, _i, _i, _i, _i]),
     "moe_debug_error": (_i32, [_vp, _vp]),
     "moe_probe_empty": (_i, [_vp]),

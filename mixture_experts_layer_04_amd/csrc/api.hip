@@ -152,7 +152,8 @@ moe_status layer_enqueue(const void* x, const void* gate, int gate_is_fp32, cons
                          const void* w13_scale, const void* w2, const void* w2_scale, int T, int H, int E, int F,
                          int k, int n_shared, int n_group, int topk_group, int scoring, int renormalize,
                          float routed_scale, int block_m, float swiglu_limit, void* y, int32_t* topk_ids_out,
-                         float* topk_weights_out, void* workspace, size_t workspace_bytes, hipStream_t stream) {
+                         float* topk_weights_out, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                         const NormArgs* norm) {
   // validate everything before enqueuing anything
   moe_status st = layer_validate(x, gate, gate_is_fp32, wformat, w13, w13_scale, w2, w2_scale, T, H, E, F, k,
                                  n_shared, n_group, topk_group, scoring, block_m, swiglu_limit, y);
@@ -184,13 +185,19 @@ moe_status layer_enqueue(const void* x, const void* gate, int gate_is_fp32, cons
   // at decode the router quantises x for the fp8 formats on the way (one
   // launch fewer)
   const int qfmt = wformat == MOE_W_FP8_BLOCK128 ? 1 : wformat == MOE_W_MXFP4 ? 2 : 0;
-  a.x_ready = qfmt != 0 && route_quantizes_x(T, E, H);
+  a.x_ready = qfmt != 0 && (norm || route_quantizes_x(T, E, H));
+  if (norm) {  // the norm leaves x normalised, and quantised for the fp8 formats
+    const moe_status ns = launch_norm(x, norm->residual, norm->residual_is_fp32, norm->weight, norm->weight_is_fp32, T,
+                                      H, norm->eps, wformat, norm->h, norm->y_norm, a.xq, a.xs, stream);
+    if (ns != MOE_OK) return ns;
+    x = a.x = norm->y_norm;
+  }
   // the alignment also writes the paired tiles' pair table where it can
   // (one launch fewer); the FFN builds it otherwise
   bool pairs_written = false;
   st = launch_route_align(x, gate, gate_is_fp32, bias, T, H, E, k, n_group, topk_group, scoring, renormalize,
                           routed_scale,
-                          n_shared, block_m, ids, w, sorted, bexp, npp, b + L.ctrl, stream, a.xq, a.xs, qfmt,
+                          n_shared, block_m, ids, w, sorted, bexp, npp, b + L.ctrl, stream, a.xq, a.xs, norm ? 0 : qfmt,
                           static_cast<int32_t*>(a.pairs), &pairs_written, /*fill_tail=*/false);
   if (st != MOE_OK) return st;
   a.pairs_ready = pairs_written;
@@ -209,6 +216,45 @@ extern "C" moe_status moe_layer(const void* x, const void* gate, int gate_is_fp3
                             n_shared, n_group,
                             topk_group, scoring, renormalize, routed_scale, block_m, swiglu_limit, y, topk_ids_out,
                             topk_weights_out, workspace, workspace_bytes, stream);
+}
+
+// moe_layer's workspace, then the normalised hidden states
+extern "C" size_t moe_norm_layer_workspace_size(int T, int H, int E, int F, int k, int n_shared, int block_m,
+                                                int wformat) {
+  const size_t layer = moe::layer_workspace_bytes(T, H, E, F, k, n_shared, block_m, wformat);
+  return layer == 0 ? 0 : layer + moe::align_up((size_t)T * H * 2, 256);
+}
+
+extern "C" moe_status moe_norm_layer(const void* x, const void* residual, int residual_is_fp32,
+                                     const void* norm_weight, int norm_weight_is_fp32, float eps, const void* gate,
+                                     int gate_is_fp32, const float* bias, int wformat, const void* w13,
+                                     const void* w13_scale, const void* w2, const void* w2_scale, int T, int H, int E,
+                                     int F, int k, int n_shared, int n_group, int topk_group, int scoring,
+                                     int renormalize, float routed_scale, int block_m, float swiglu_limit, void* h,
+                                     void* y, int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
+                                     size_t workspace_bytes, hipStream_t stream) {
+  using namespace moe;
+  uint8_t dummy = 0;
+  moe_status st = layer_validate(x, gate, gate_is_fp32, wformat, w13, w13_scale, w2, w2_scale, T, H, E, F, k, n_shared,
+                                 n_group, topk_group, scoring, block_m, swiglu_limit, y);
+  if (st != MOE_OK) return st;
+  st = norm_validate(x, residual, residual_is_fp32, norm_weight, norm_weight_is_fp32, T, H, eps, wformat, h, &dummy,
+                     &dummy, &dummy);
+  if (st != MOE_OK || T == 0) return st;
+  if (!workspace) return MOE_E_INVAL;
+  const size_t layer = layer_workspace_bytes(T, H, E, F, k, n_shared, block_m, wformat);
+  if (workspace_bytes < layer + align_up((size_t)T * H * 2, 256)) return MOE_E_WORKSPACE;
+  NormArgs n;
+  n.residual = residual;
+  n.residual_is_fp32 = residual_is_fp32;
+  n.weight = norm_weight;
+  n.weight_is_fp32 = norm_weight_is_fp32;
+  n.eps = eps;
+  n.h = h;
+  n.y_norm = static_cast<char*>(workspace) + layer;
+  return layer_enqueue(x, gate, gate_is_fp32, bias, wformat, w13, w13_scale, w2, w2_scale, T, H, E, F, k, n_shared,
+                       n_group, topk_group, scoring, renormalize, routed_scale, block_m, swiglu_limit, y, topk_ids_out,
+                       topk_weights_out, workspace, layer, stream, &n);
 }
 
 extern "C" int32_t moe_debug_error(void* workspace, hipStream_t stream) {

@@ -1,0 +1,647 @@
+// moe_balance_loss and moe_route_grad: the router's training side.
+//
+// With sc the scores of a token's logits (softmax, sigmoid or
+// sqrt(softplus), as moe_route takes them), p = sc / sum(sc) (softmax: p =
+// sc), c[s, e] the assignments of sequence s to expert e, n_s its tokens and
+// S' the sequences that have any:
+//
+//   balance = 1/S' sum_s sum_e (E c[s,e] / (k n_s)) (1/n_s sum_t p[t,e])
+//   z       = 1/N sum_t logsumexp(l_t)^2            (N = sum_s n_s)
+//
+// Gradient to the logits, with gb = d_balance E c / (k n_s^2 S') (the counts
+// carry no gradient) and gw the gradient of the routing weights w_j =
+// scale sc_j / (sum_sel sc + 1e-20) (or scale sc_j) on the scores:
+//
+//   softmax:    d = p (g - sum p g),  g = gb + gw
+//   the others: d = sc' ((gb - sum p gb) / sum(sc) + gw)
+//   both:       d += d_z 2/N lse softmax(l)
+//
+// A token's E logits sit in the registers of 16 neighbouring lanes (64 above
+// 512 experts), so the row sums are four DPP steps and a wave holds four
+// tokens.  The column sums of the loss are accumulated per lane over the
+// tokens of a run, then added across lanes, waves and runs in a fixed order;
+// only integer counts use atomics, so every result is the same in every run.
+
+#include <cmath>
+
+#include "common.h"
+#include "launch.h"
+
+namespace moe {
+
+namespace {
+
+constexpr int kMaxSeqs = 1 << 20;
+constexpr float kTiny = 1e-20f;  // the guard of the router's own renormalisation
+constexpr float kNegInf = -__builtin_huge_valf();
+
+__device__ __forceinline__ float row_sum16(float v) {
+  v = v + dpp_f32<0xB1>(v);
+  v = v + dpp_f32<0x4E>(v);
+  v = v + dpp_f32<0x141>(v);
+  return v + dpp_f32<0x140>(v);
+}
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+  return LANES == 16 ? row_sum16(v) : wave_sum_u(v);
+}
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+  return LANES == 16 ? row_max16(v) : wave_max_u(v);
+}
+
+// 4 logits from expert e on; -inf (a score of zero) past the last expert
+__device__ __forceinline__ void load4(const float* row, int e, int E, float* l) {
+  if (e + 4 <= E) {
+    f32x4_t v;
+    __builtin_memcpy(&v, row + e, 16);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) l[j] = v[j];
+  } else {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) l[j] = e + j < E ? row[e + j] : kNegInf;
+  }
+}
+
+// Score and its derivative by the logit (sigmoid and sqrt(softplus)).  With
+// t = exp(-|l|) <= 1 nothing overflows, and 1 - sigmoid is not formed by a
+// subtraction.
+template <int SC>
+__device__ __forceinline__ float score(float l) {
+  const float t = expf(-fabsf(l));
+  if (SC == MOE_SIGMOID) return (l >= 0.f ? 1.f : t) / (1.f + t);
+  return sqrtf(fmaxf(l, 0.f) + log1pf(t));
+}
+template <int SC>
+__device__ __forceinline__ float score_and_slope(float l, float& slope) {
+  const float t = expf(-fabsf(l)), r = 1.f / (1.f + t);
+  if (SC == MOE_SIGMOID) {
+    slope = t * r * r;
+    return l >= 0.f ? r : t * r;
+  }
+  const float s = sqrtf(fmaxf(l, 0.f) + log1pf(t));
+  slope = s > 0.f ? (l >= 0.f ? r : t * r) / (2.f * s) : 0.f;
+  return s;
+}
+
+// Sequence boundaries are read on the device and clamped to the batch, so
+// that no value of theirs leads outside a buffer.
+__device__ __forceinline__ int seq_at(const int32_t* off, int s, int T) {
+  const int v = off[s];
+  return v < 0 ? 0 : v > T ? T : v;
+}
+// first s of [0, S) whose end lies past row t (S - 1 if none does)
+__device__ __forceinline__ int seq_of(const int32_t* off, int S, int T, int t) {
+  int lo = 0, hi = S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (seq_at(off, mid + 1, T) > t)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return lo;
+}
+
+struct BalanceP {
+  const float* logits;
+  const int32_t* ids;
+  const uint8_t* mask;
+  const int32_t* off;
+  int T, E, k, ks, S;
+  int chunk, chunks;  // rows per workgroup, and how many
+  int Ep;             // E padded to 64: row length of the partial sums
+  // per piece (a run of one sequence's rows inside one chunk; piece (c, s)
+  // has slot c + s, no two pieces the same one)
+  float* psum;    // [slots][Ep]
+  int32_t* csum;  // [slots][Ep]
+  float* zsum;    // [slots]
+  int32_t* nsum;  // [slots]
+  // per sequence
+  float* dot;    // [S][Ep / 64]
+  float* zseq;   // [S]
+  int32_t* nseq;  // [S]: the tokens output
+  float* losses;
+  int32_t* counts;
+  float* probs;
+};
+
+// One workgroup per chunk of rows: the pieces of the sequences in it.
+template <int LANES, int NV, int SC>
+__global__ __launch_bounds__(256) void balance_kernel(BalanceP p) {
+  constexpr int V = 4 * NV, GROUPS = 256 / LANES;
+  extern __shared__ float lds[];  // [4][Ep] column sums per wave, then [Ep] counts
+  int32_t* hist = reinterpret_cast<int32_t*>(lds + 4 * p.Ep);
+  __shared__ float zw[4];
+  __shared__ int nw[4];
+  const int j = threadIdx.x % LANES, g = threadIdx.x / LANES, wave = threadIdx.x >> 6;
+  const int a = blockIdx.x * p.chunk, b = min(p.T, a + p.chunk);
+  int s = p.off ? seq_of(p.off, p.S, p.T, a) : 0;
+  for (; s < p.S; ++s) {
+    const int lo = p.off ? max(a, seq_at(p.off, s, p.T)) : a;
+    const int hi = p.off ? min(b, seq_at(p.off, s + 1, p.T)) : b;
+    if (lo >= b) break;
+    if (lo >= hi) continue;
+    for (int e = threadIdx.x; e < p.Ep; e += 256) hist[e] = 0;
+    __syncthreads();
+    for (int i = threadIdx.x; i < (hi - lo) * p.k; i += 256) {
+      const int t = lo + i / p.k;
+      if (p.mask && !p.mask[t]) continue;
+      const int id = p.ids[(size_t)t * p.ks + i % p.k];
+      if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+    }
+    float acc[V], z = 0.f;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int t = lo + g; t < hi; t += GROUPS) {
+      if (p.mask && !p.mask[t]) continue;
+      float l[V];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) load4(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, l + 4 * v);
+      float m = kNegInf;
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+      m = group_max<LANES>(m);
+      if (m == kNegInf) m = 0.f;  // every logit -inf: the sum below is zero
+      float e[V], es = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        e[i] = expf(l[i] - m);
+        es += e[i];
+      }
+      es = group_sum<LANES>(es);
+      float tot = es;
+      if (SC != MOE_SOFTMAX) {
+        tot = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          e[i] = score<SC>(l[i]);
+          tot += e[i];
+        }
+        tot = group_sum<LANES>(tot) + kTiny;
+      }
+      const float inv = tot == 0.f ? 0.f : 1.f / tot, lse = es == 0.f ? 0.f : m + logf(es);
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += e[i] * inv;
+      z += lse * lse;
+      ++n;
+    }
+    if (LANES == 16) {  // the wave's four tokens
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        acc[i] += __shfl_xor(acc[i], 16, kWave);
+        acc[i] += __shfl_xor(acc[i], 32, kWave);
+      }
+      z += __shfl_xor(z, 16, kWave);
+      z += __shfl_xor(z, 32, kWave);
+      n += __shfl_xor(n, 16, kWave);
+      n += __shfl_xor(n, 32, kWave);
+    }
+    if ((threadIdx.x & 63) < LANES) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = ((i / 4) * LANES + j) * 4 + i % 4;
+        if (e < p.Ep) lds[wave * p.Ep + e] = acc[i];
+      }
+      if (j == 0) {
+        zw[wave] = z;
+        nw[wave] = n;
+      }
+    }
+    __syncthreads();
+    const size_t slot = (size_t)blockIdx.x + s;
+    for (int e = threadIdx.x; e < p.Ep; e += 256) {
+      p.psum[slot * p.Ep + e] = (lds[e] + lds[p.Ep + e]) + (lds[2 * p.Ep + e] + lds[3 * p.Ep + e]);
+      p.csum[slot * p.Ep + e] = hist[e];
+    }
+    if (threadIdx.x == 0) {
+      p.zsum[slot] = (zw[0] + zw[1]) + (zw[2] + zw[3]);
+      p.nsum[slot] = nw[0] + nw[1] + nw[2] + nw[3];
+    }
+    __syncthreads();
+  }
+}
+
+// Grid (sequences, Ep / 64), 1024 threads: adds the pieces of a sequence for
+// 64 experts (64 slices of the pieces, then the slices), writes its counts
+// and mean probabilities, and this tile's share of sum_e c P.
+__global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceP p) {
+  __shared__ float ps[64][64];
+  __shared__ int32_t cs[64][64];
+  __shared__ float zs[16];
+  __shared__ int ns[16];
+  const int s = blockIdx.x, wave = threadIdx.x >> 6;
+  const int lo = p.off ? seq_at(p.off, s, p.T) : 0, hi = p.off ? seq_at(p.off, s + 1, p.T) : p.T;
+  const int first = lo / p.chunk, last = hi > lo ? (hi - 1) / p.chunk : first - 1;
+  const int quad = threadIdx.x & 15, slice = threadIdx.x >> 4;
+  const int e0 = blockIdx.y * 64;
+  f32x4_t pa = {0.f, 0.f, 0.f, 0.f};
+  i32x4_t ca = {0, 0, 0, 0};
+  for (int c = first + slice; c <= last; c += 64) {
+    const size_t at = (size_t)(c + s) * p.Ep + e0 + quad * 4;
+    pa += *reinterpret_cast<const f32x4_t*>(p.psum + at);
+    ca += *reinterpret_cast<const i32x4_t*>(p.csum + at);
+  }
+  float z = 0.f;
+  int n = 0;
+  for (int c = first + (int)threadIdx.x; c <= last; c += 1024) {
+    z += p.zsum[c + s];
+    n += p.nsum[c + s];
+  }
+  z = wave_sum(z);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
+  if ((threadIdx.x & 63) == 0) {
+    zs[wave] = z;
+    ns[wave] = n;
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    ps[slice][quad * 4 + i] = pa[i];
+    cs[slice][quad * 4 + i] = ca[i];
+  }
+  __syncthreads();
+  if (threadIdx.x < 64) {
+    n = 0;
+    z = 0.f;
+    for (int i = 0; i < 16; ++i) {
+      n += ns[i];
+      z += zs[i];
+    }
+    float P = 0.f;
+    int c = 0;
+#pragma unroll 8
+    for (int i = 0; i < 64; ++i) {
+      P += ps[i][threadIdx.x];
+      c += cs[i][threadIdx.x];
+    }
+    P = n > 0 ? P / (float)n : 0.f;
+    const int e = e0 + threadIdx.x;
+    if (e < p.E) {
+      p.probs[(size_t)s * p.E + e] = P;
+      p.counts[(size_t)s * p.E + e] = c;
+    }
+    const float f = n > 0 ? (float)c / (float)n * ((float)p.E / (float)p.k) : 0.f;
+    const float d = wave_sum(f * P);
+    if (threadIdx.x == 0) {
+      p.dot[(size_t)s * gridDim.y + blockIdx.y] = d;
+      if (blockIdx.y == 0) {
+        p.zseq[s] = z;
+        p.nseq[s] = n;
+      }
+    }
+  }
+}
+
+// One workgroup: the losses from the sequences' shares, and the token and
+// sequence numbers behind the per-sequence ones.
+__global__ __launch_bounds__(256) void balance_total_kernel(BalanceP p, int tiles) {
+  __shared__ double bs[256], zs[256];
+  __shared__ int ns[256], fs[256];
+  double b = 0.0, z = 0.0;
+  int n = 0, full = 0;
+  for (int s = threadIdx.x; s < p.S; s += 256) {
+    for (int i = 0; i < tiles; ++i) b += (double)p.dot[(size_t)s * tiles + i];
+    z += (double)p.zseq[s];
+    n += p.nseq[s];
+    full += p.nseq[s] > 0;
+  }
+  bs[threadIdx.x] = b;
+  zs[threadIdx.x] = z;
+  ns[threadIdx.x] = n;
+  fs[threadIdx.x] = full;
+  __syncthreads();
+  for (int w = 128; w >= 1; w >>= 1) {
+    if ((int)threadIdx.x < w) {
+      bs[threadIdx.x] += bs[threadIdx.x + w];
+      zs[threadIdx.x] += zs[threadIdx.x + w];
+      ns[threadIdx.x] += ns[threadIdx.x + w];
+      fs[threadIdx.x] += fs[threadIdx.x + w];
+    }
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) {
+    p.losses[0] = fs[0] ? (float)(bs[0] / fs[0]) : 0.f;
+    p.losses[1] = ns[0] ? (float)(zs[0] / ns[0]) : 0.f;
+    p.nseq[p.S] = ns[0];
+    p.nseq[p.S + 1] = fs[0];
+  }
+}
+
+struct RouteGradP {
+  const float* logits;
+  const int32_t* ids;
+  const uint8_t* mask;
+  const int32_t* off;
+  const float* d_weights;  // optional [T][ks]
+  const float* d_losses;   // optional [2]
+  const int32_t* counts;
+  const int32_t* tokens;
+  float* out;
+  int T, E, k, ks, S, renorm;
+  float scale;
+};
+
+template <int LANES, int NV, int SC>
+__global__ __launch_bounds__(256) void route_grad_kernel(RouteGradP p) {
+  constexpr int V = 4 * NV, GROUPS = 256 / LANES, ROW = NV * LANES * 4;
+  __shared__ float gwbuf[GROUPS * ROW];  // gradient of the chosen scores, by expert; zero between tokens
+  const int j = threadIdx.x % LANES, g = threadIdx.x / LANES;
+  float* gwrow = gwbuf + g * ROW;
+#pragma unroll
+  for (int v = 0; v < NV; ++v) *reinterpret_cast<f32x4_t*>(gwrow + (v * LANES + j) * 4) = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  const float da = p.d_losses ? p.d_losses[0] : 0.f, dz = p.d_losses ? p.d_losses[1] : 0.f;
+  const float total = p.d_losses ? (float)p.tokens[p.S] : 1.f, full = p.d_losses ? (float)p.tokens[p.S + 1] : 1.f;
+  for (int t0 = blockIdx.x * GROUPS; t0 < p.T; t0 += gridDim.x * GROUPS) {
+    const int t = t0 + g;
+    if (t >= p.T) continue;
+    // the losses' part: rows of a sequence that the mask keeps
+    bool loss = p.d_losses != nullptr && !(p.mask && !p.mask[t]);
+    int s = 0;
+    if (loss && p.off) {
+      s = seq_of(p.off, p.S, p.T, t);
+      loss = seq_at(p.off, s, p.T) <= t && t < seq_at(p.off, s + 1, p.T);
+    }
+    // the weights' part: slot j of the token on lane j
+    int id = -1;
+    float dw = 0.f;
+    if (p.d_weights && j < p.k) {
+      id = p.ids[(size_t)t * p.ks + j];
+      if (id < 0 || id >= p.E)
+        id = -1;
+      else
+        dw = p.d_weights[(size_t)t * p.ks + j] * p.scale;
+    }
+    const bool weights = group_max<LANES>(dw != 0.f ? 1.f : 0.f) > 0.f;  // NaN counts
+    float* out = p.out + (size_t)t * p.E;
+    float d[V];
+    if (!loss && !weights) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) d[i] = 0.f;
+    } else {
+      const float* row = p.logits + (size_t)t * p.E;
+      float l[V];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) load4(row, (v * LANES + j) * 4, p.E, l + 4 * v);
+      float m = kNegInf;
+#pragma unroll
+      for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+      m = group_max<LANES>(m);
+      if (m == kNegInf) m = 0.f;
+      float soft[V], es = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        soft[i] = expf(l[i] - m);
+        es += soft[i];
+      }
+      es = group_sum<LANES>(es);
+      const float einv = es == 0.f ? 0.f : 1.f / es, lse = es == 0.f ? 0.f : m + logf(es);
+#pragma unroll
+      for (int i = 0; i < V; ++i) soft[i] *= einv;
+      float sc[V], slope[V], tot = 0.f;
+      if (SC != MOE_SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          sc[i] = score_and_slope<SC>(l[i], slope[i]);
+          tot += sc[i];
+        }
+        tot = group_sum<LANES>(tot) + kTiny;
+      }
+      float gw[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) gw[i] = 0.f;
+      if (weights) {
+        float sel = 0.f;
+        if (id >= 0) sel = SC == MOE_SOFTMAX ? expf(row[id] - m) * einv : score<SC>(row[id]);
+        float ds = dw;
+        if (p.renorm) {
+          const float den = group_sum<LANES>(sel) + kTiny;
+          ds = (dw - group_sum<LANES>(id >= 0 ? dw * sel : 0.f) / den) / den;
+        }
+        // slots that chose the same expert: each gets the sum of all of them
+        float sum = 0.f;
+        for (int i = 0; i < p.k; ++i) {
+          const int oid = __shfl(id, i, LANES);
+          const float od = __shfl(ds, i, LANES);
+          if (oid == id) sum += od;
+        }
+        if (id >= 0) gwrow[id] = sum;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int v = 0; v < NV; ++v) {
+          const f32x4_t x = *reinterpret_cast<const f32x4_t*>(gwrow + (v * LANES + j) * 4);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) gw[4 * v + i] = x[i];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (id >= 0) gwrow[id] = 0.f;
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+      float gb[V], beta = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) gb[i] = 0.f;
+      if (loss) {
+        const float n = (float)p.tokens[s];
+        const float alpha = da * ((float)p.E / (float)p.k) / (n * n * full);
+        beta = dz * 2.f / total * lse;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = ((i / 4) * LANES + j) * 4 + i % 4;
+          if (e < p.E) gb[i] = alpha * (float)p.counts[(size_t)s * p.E + e];
+        }
+      }
+      float dot = 0.f;
+      if (SC == MOE_SOFTMAX) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot += soft[i] * (gb[i] + gw[i]);
+        dot = group_sum<LANES>(dot);
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = soft[i] * ((gb[i] + gw[i]) - dot + beta);
+      } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) dot += sc[i] * gb[i];
+        dot = group_sum<LANES>(dot) / tot;
+#pragma unroll
+        for (int i = 0; i < V; ++i) d[i] = slope[i] * ((gb[i] - dot) / tot + gw[i]) + beta * soft[i];
+      }
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      const int e = (v * LANES + j) * 4;
+      if (e + 4 <= p.E) {
+        const f32x4_t x = {d[4 * v], d[4 * v + 1], d[4 * v + 2], d[4 * v + 3]};
+        __builtin_memcpy(out + e, &x, 16);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (e + i < p.E) out[e + i] = d[4 * v + i];
+      }
+    }
+  }
+}
+
+// Rows per workgroup of the loss: at most 1024 chunks, none below 16 rows.
+int balance_chunk(int T) { return T <= 16 * 1024 ? 16 : ceil_div(ceil_div(T, 1024), 16) * 16; }
+
+struct BalanceLayout {
+  size_t psum, csum, zsum, nsum, dot, zseq, total;
+};
+BalanceLayout balance_layout(int T, int E, int S) {
+  const size_t Ep = align_up((size_t)E, 64);
+  const size_t slots = (size_t)ceil_div(T, balance_chunk(T)) + S;
+  BalanceLayout L;
+  size_t off = kCtrlBytes;  // the control block stays as it is
+  auto take = [&](size_t bytes) {
+    const size_t at = off;
+    off += align_up(bytes, 256);
+    return at;
+  };
+  L.psum = take(slots * Ep * 4);
+  L.csum = take(slots * Ep * 4);
+  L.zsum = take(slots * 4);
+  L.nsum = take(slots * 4);
+  L.dot = take((size_t)S * (Ep / 64) * 4);
+  L.zseq = take((size_t)S * 4);
+  L.total = off;
+  return L;
+}
+
+moe_status router_shape(int T, int E, int k, int n_shared, int n_seq, int scoring) {
+  if (T < 0 || T > (1 << 24) || E < 1 || E > 1024 || k < 1 || k > E || k > 16) return MOE_E_INVAL;
+  if (n_shared < 0 || n_shared > 1 || k + n_shared > 16) return MOE_E_INVAL;
+  if (n_seq < 1 || n_seq > kMaxSeqs) return MOE_E_INVAL;
+  if (scoring != MOE_SOFTMAX && scoring != MOE_SIGMOID && scoring != MOE_SQRTSOFTPLUS) return MOE_E_INVAL;
+  return MOE_OK;
+}
+
+template <int LANES, int NV>
+void balance_launch(const BalanceP& p, int scoring, hipStream_t s) {
+  const size_t lds = (size_t)5 * p.Ep * 4;
+  switch (scoring) {
+    case MOE_SOFTMAX: balance_kernel<LANES, NV, MOE_SOFTMAX><<<p.chunks, 256, lds, s>>>(p); break;
+    case MOE_SIGMOID: balance_kernel<LANES, NV, MOE_SIGMOID><<<p.chunks, 256, lds, s>>>(p); break;
+    default: balance_kernel<LANES, NV, MOE_SQRTSOFTPLUS><<<p.chunks, 256, lds, s>>>(p); break;
+  }
+}
+template <int LANES, int NV>
+void route_grad_launch(const RouteGradP& p, int scoring, hipStream_t s) {
+  const int64_t need = ceil_div64(p.T, 256 / LANES);
+  const int grid = (int)(need < 4096 ? need : 4096);
+  switch (scoring) {
+    case MOE_SOFTMAX: route_grad_kernel<LANES, NV, MOE_SOFTMAX><<<grid, 256, 0, s>>>(p); break;
+    case MOE_SIGMOID: route_grad_kernel<LANES, NV, MOE_SIGMOID><<<grid, 256, 0, s>>>(p); break;
+    default: route_grad_kernel<LANES, NV, MOE_SQRTSOFTPLUS><<<grid, 256, 0, s>>>(p); break;
+  }
+}
+
+// 16 lanes per token up to 512 experts (4 per lane and 64 of them), else 64
+#define MOE_BY_EXPERTS(FN, E, ...)                  \
+  do {                                              \
+    switch (ceil_div(E, 64)) {                      \
+      case 1: FN<16, 1>(__VA_ARGS__); break;        \
+      case 2: FN<16, 2>(__VA_ARGS__); break;        \
+      case 3: FN<16, 3>(__VA_ARGS__); break;        \
+      case 4: FN<16, 4>(__VA_ARGS__); break;        \
+      case 5: FN<16, 5>(__VA_ARGS__); break;        \
+      case 6: FN<16, 6>(__VA_ARGS__); break;        \
+      case 7: case 8: FN<16, 8>(__VA_ARGS__); break; \
+      case 9: case 10: case 11: case 12: FN<64, 3>(__VA_ARGS__); break; \
+      default: FN<64, 4>(__VA_ARGS__); break;       \
+    }                                               \
+  } while (0)
+
+}  // namespace
+
+}  // namespace moe
+
+extern "C" size_t moe_balance_loss_workspace_size(int T, int E, int n_seq) {
+  if (T < 0 || T > (1 << 24) || E < 1 || E > 1024 || n_seq < 1 || n_seq > moe::kMaxSeqs) return 0;
+  return moe::balance_layout(T, E, n_seq).total;
+}
+
+extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask,
+                                       const int32_t* seq_offsets, int T, int E, int k, int n_shared, int n_seq,
+                                       int scoring, float* losses, int32_t* counts, float* probs, int32_t* tokens,
+                                       void* workspace, size_t workspace_bytes, hipStream_t stream) {
+  using namespace moe;
+  const moe_status st = router_shape(T, E, k, n_shared, n_seq, scoring);
+  if (st != MOE_OK) return st;
+  if (!seq_offsets && n_seq != 1) return MOE_E_INVAL;
+  if (T > 0 && (!logits || !topk_ids)) return MOE_E_INVAL;
+  if (!losses || !counts || !probs || !tokens || !workspace) return MOE_E_INVAL;
+  const BalanceLayout L = balance_layout(T, E, n_seq);
+  if (workspace_bytes < L.total) return MOE_E_WORKSPACE;
+  char* b = static_cast<char*>(workspace);
+  BalanceP p;
+  p.logits = logits;
+  p.ids = topk_ids;
+  p.mask = token_mask;
+  p.off = seq_offsets;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.ks = k + n_shared;
+  p.S = n_seq;
+  p.chunk = balance_chunk(T);
+  p.chunks = ceil_div(T, p.chunk);
+  p.Ep = (int)align_up((size_t)E, 64);
+  p.psum = reinterpret_cast<float*>(b + L.psum);
+  p.csum = reinterpret_cast<int32_t*>(b + L.csum);
+  p.zsum = reinterpret_cast<float*>(b + L.zsum);
+  p.nsum = reinterpret_cast<int32_t*>(b + L.nsum);
+  p.dot = reinterpret_cast<float*>(b + L.dot);
+  p.zseq = reinterpret_cast<float*>(b + L.zseq);
+  p.nseq = tokens;
+  p.losses = losses;
+  p.counts = counts;
+  p.probs = probs;
+  if (T > 0) {
+    MOE_BY_EXPERTS(balance_launch, E, p, scoring, stream);
+    MOE_CHECK_LAUNCH();
+  }
+  const dim3 grid((unsigned)n_seq, (unsigned)(p.Ep / 64));
+  balance_seq_kernel<<<grid, 1024, 0, stream>>>(p);
+  MOE_CHECK_LAUNCH();
+  balance_total_kernel<<<1, 256, 0, stream>>>(p, p.Ep / 64);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}
+
+extern "C" moe_status moe_route_grad(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask,
+                                     const int32_t* seq_offsets, int T, int E, int k, int n_shared, int n_seq,
+                                     int scoring, int renormalize, float routed_scale, const float* d_weights,
+                                     const float* d_losses, const int32_t* counts, const int32_t* tokens,
+                                     float* d_logits, hipStream_t stream) {
+  using namespace moe;
+  const moe_status st = router_shape(T, E, k, n_shared, n_seq, scoring);
+  if (st != MOE_OK) return st;
+  if (!seq_offsets && n_seq != 1) return MOE_E_INVAL;
+  if (!d_weights && !d_losses) return MOE_E_INVAL;
+  if (d_losses && (!counts || !tokens)) return MOE_E_INVAL;
+  if (T == 0) return MOE_OK;
+  if (!logits || !topk_ids || !d_logits) return MOE_E_INVAL;
+  RouteGradP p;
+  p.logits = logits;
+  p.ids = topk_ids;
+  p.mask = token_mask;
+  p.off = seq_offsets;
+  p.d_weights = d_weights;
+  p.d_losses = d_losses;
+  p.counts = counts;
+  p.tokens = tokens;
+  p.out = d_logits;
+  p.T = T;
+  p.E = E;
+  p.k = k;
+  p.ks = k + n_shared;
+  p.S = n_seq;
+  p.renorm = renormalize != 0;
+  p.scale = routed_scale;
+  MOE_BY_EXPERTS(route_grad_launch, E, p, scoring, stream);
+  MOE_CHECK_LAUNCH();
+  return MOE_OK;
+}

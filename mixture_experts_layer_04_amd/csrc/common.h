@@ -32,6 +32,14 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return f32_to_bf16_bits(lo) | (f32_to_bf16_bits(hi) << 16);
 }
 
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+// two fp32 -> packed bf16, ties to even, NaN kept (v_cvt_pk_bf16_f32)
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2_t));
+}
+
 // Order-preserving map of an fp32 value to uint32 (larger float -> larger
 // unsigned); used to reduce (key, id) pairs with one integer max.
 __device__ __forceinline__ uint32_t f32_order_key(float f) {

@@ -109,6 +109,15 @@ moe_status launch_gemm_mxfp4(const FfnArgs& a, int which, hipStream_t stream);
 moe_status launch_quant_x(const FfnArgs& a, hipStream_t stream);
 moe_status launch_finalize(const FfnArgs& a, hipStream_t stream);
 
+// The norm in front of the layer (norm.hip): qformat is the moe_wformat whose
+// activation format q / s take (MOE_W_BF16: none).
+moe_status norm_validate(const void* x, const void* residual, int residual_is_fp32, const void* weight,
+                         int weight_is_fp32, int T, int H, float eps, int qformat, const void* h, const void* y,
+                         const void* q, const void* s);
+moe_status launch_norm(const void* x, const void* residual, int residual_is_fp32, const void* weight,
+                       int weight_is_fp32, int T, int H, float eps, int qformat, void* h, void* y, void* q, void* s,
+                       hipStream_t stream);
+
 // Grid size for a grid-stride loop over `n_tiles` tiles that are spread over
 // the 8 XCDs in contiguous runs (see xcd_tile()).
 int tile_grid(int64_t n_tiles, int max_wgs);
@@ -120,12 +129,24 @@ moe_status layer_validate(const void* x, const void* gate, int gate_is_fp32, int
                           const void* w13_scale,
                           const void* w2, const void* w2_scale, int T, int H, int E, int F, int k, int n_shared,
                           int n_group, int topk_group, int scoring, int block_m, float swiglu_limit, const void* y);
+// norm (optional): x and the residual are normalised first, into y_norm
+// (bf16 [T, H]) and, for the fp8 formats, straight into the FFN's xq / xs.
+struct NormArgs {
+  const void* residual;
+  int residual_is_fp32;
+  const void* weight;
+  int weight_is_fp32;
+  float eps;
+  void* h;
+  void* y_norm;
+};
 moe_status layer_enqueue(const void* x, const void* gate, int gate_is_fp32, const float* bias, int wformat,
                          const void* w13,
                          const void* w13_scale, const void* w2, const void* w2_scale, int T, int H, int E, int F,
                          int k, int n_shared, int n_group, int topk_group, int scoring, int renormalize,
                          float routed_scale, int block_m, float swiglu_limit, void* y, int32_t* topk_ids_out,
-                         float* topk_weights_out, void* workspace, size_t workspace_bytes, hipStream_t stream);
+                         float* topk_weights_out, void* workspace, size_t workspace_bytes, hipStream_t stream,
+                         const NormArgs* norm = nullptr);
 
 }  // namespace moe
 

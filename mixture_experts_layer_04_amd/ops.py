@@ -6,7 +6,11 @@ include/moe.h: x bf16 [T, H]; gate float32 or bf16 [E, H] (the dtype sets
 gate_is_fp32); bias float32 [E] or None;
 w13 / w2 in the layout of the weight format (bf16, or uint8 codes plus
 float32 (fp8) / uint8 e8m0 (mxfp4) scales).  Work goes onto the current
-stream.  The workspace is a zero-initialised byte tensor cached per device
+stream of the tensors' device.  The norm and the router's training side
+(rms_norm, rms_norm_grad, balance_loss, route_grad, gate_grad) check shapes,
+types and devices and raise ValueError; where they need scratch memory they
+take it from torch's allocator per call, so calls on several streams and in
+several captured graphs do not meet in it.  Everywhere else the workspace is a zero-initialised byte tensor cached per device
 (or passed in); calls that overlap in time must not share one.
 """
 
@@ -217,6 +221,262 @@ def layer_noalloc(x, gate, bias, w13, w2, k, scoring="softmax", n_group=1, topk_
                                   _stream(x.device)),
           "moe_layer_noalloc")
     return (y, ids, w) if return_routing else y
+
+
+# ---------------------------------------------------------------------------
+# the norm in front of the layer, and the router's training side
+
+_TYPE_IS_FP32 = {torch.float32: 1, torch.bfloat16: 0}
+
+
+def _tensor(name, t, dtypes, shape, device):
+    """Checks one argument (a dtype or a tuple of them; the shape)."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name}: libmoe ops take GPU tensors of one device, not {t.device}")
+    if t.dtype != dtypes and not (isinstance(dtypes, tuple) and t.dtype in dtypes):
+        raise ValueError(f"{name} has type {t.dtype}, not {dtypes}")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: libmoe ops take contiguous tensors")
+
+
+def _call(name, device, *args):
+    """One library call on the current stream of ``device``, with that
+    device current while the kernels are launched."""
+    fn = getattr(lib(), name)
+    if torch.cuda.current_device() != device.index:
+        with torch.cuda.device(device):
+            check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+    else:
+        check(fn(*args, torch.cuda.current_stream(device).cuda_stream), name)
+
+
+_BF16_FP32 = (torch.bfloat16, torch.float32)
+
+
+def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=None, s=None, with_y=True):
+    """moe_rms_norm -> (y, h), or (y, h, q, s) with ``quant``.
+
+    y bf16 [T, H]: the norm of x + residual (None with quant and
+    ``with_y=False``); h: x + residual in the residual's type (None without
+    a residual: it is x).  ``quant`` "fp8" or "mxfp4": also the activations
+    of those expert formats, q uint8 [T, H] (e4m3 codes) and s float32
+    [T, H/128] or uint8 [T, H/32] (e8m0).  Outputs are allocated unless
+    given; h may be the residual (in place)."""
+    if x.dim() != 2:
+        raise ValueError(f"x has shape {tuple(x.shape)}, not [T, H]")
+    T, H = x.shape
+    dev = x.device
+    _tensor("x", x, torch.bfloat16, (T, H), dev)
+    _tensor("weight", weight, _BF16_FP32, (H,), dev)
+    if quant not in (None, "fp8", "mxfp4"):
+        raise ValueError(f"quant is None, 'fp8' or 'mxfp4', not {quant!r}")
+    rf = 0
+    if residual is not None:
+        _tensor("residual", residual, _BF16_FP32, (T, H), dev)
+        rf = _TYPE_IS_FP32[residual.dtype]
+        if h is None:
+            h = torch.empty_like(residual)
+        else:
+            _tensor("h", h, residual.dtype, (T, H), dev)
+    elif h is not None:
+        raise ValueError("h without a residual is x")
+    if y is not None:
+        _tensor("y", y, torch.bfloat16, (T, H), dev)
+    elif with_y or quant is None:
+        y = torch.empty_like(x)
+    if quant is None:
+        if q is not None or s is not None:
+            raise ValueError("q and s are outputs of a quantised norm")
+        qf = 0
+    else:
+        qf = WFORMAT[quant]
+        group, st = (128, torch.float32) if quant == "fp8" else (32, torch.uint8)
+        if H % group:
+            raise ValueError(f"H = {H} is not a multiple of the {quant} group of {group}")
+        if q is None:
+            q = torch.empty((T, H), dtype=torch.uint8, device=dev)
+        else:
+            _tensor("q", q, torch.uint8, (T, H), dev)
+        if s is None:
+            s = torch.empty((T, H // group), dtype=st, device=dev)
+        else:
+            _tensor("s", s, st, (T, H // group), dev)
+    _call("moe_rms_norm", dev, x.data_ptr(), _ptr(residual), rf, weight.data_ptr(), _TYPE_IS_FP32[weight.dtype], T, H,
+          eps, qf, _ptr(h), _ptr(y), _ptr(q), _ptr(s))
+    return (y, h) if quant is None else (y, h, q, s)
+
+
+def rms_norm_grad(dy, h, weight, eps=1e-6, dh=None, dx=None, with_weight=True):
+    """moe_rms_norm_grad -> (dx, d_weight): the gradients of x (and of the
+    residual) in h's type and of the weight in float32 (None without
+    ``with_weight``).  ``h``: the forward call's h, or its x where it had no
+    residual; ``dh``: the gradient that reaches h from elsewhere."""
+    if dy.dim() != 2:
+        raise ValueError(f"dy has shape {tuple(dy.shape)}, not [T, H]")
+    T, H = dy.shape
+    dev = dy.device
+    _tensor("dy", dy, torch.bfloat16, (T, H), dev)
+    _tensor("h", h, _BF16_FP32, (T, H), dev)
+    _tensor("weight", weight, _BF16_FP32, (H,), dev)
+    if dh is not None:
+        _tensor("dh", dh, h.dtype, (T, H), dev)
+    if dx is None:
+        dx = torch.empty_like(h)
+    else:
+        _tensor("dx", dx, h.dtype, (T, H), dev)
+    dw = ws = None
+    need = 0
+    if with_weight:
+        dw = torch.empty(H, dtype=torch.float32, device=dev)
+        need = lib().moe_rms_norm_grad_workspace_size(T, H)
+        ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call("moe_rms_norm_grad", dev, dy.data_ptr(), _ptr(dh), h.data_ptr(), _TYPE_IS_FP32[h.dtype], weight.data_ptr(),
+          _TYPE_IS_FP32[weight.dtype], T, H, eps, dx.data_ptr(), _ptr(dw), _ptr(ws), need)
+    return dx, dw
+
+
+def _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask):
+    """Checks what balance_loss and route_grad share; (T, E, k, sequences)."""
+    if logits.dim() != 2 or topk_ids.dim() != 2:
+        raise ValueError("logits are [T, E] and topk_ids [T, k]")
+    T, E = logits.shape
+    dev = logits.device
+    _tensor("logits", logits, torch.float32, (T, E), dev)
+    _tensor("topk_ids", topk_ids, torch.int32, (T, topk_ids.shape[1]), dev)
+    n_seq = 1
+    if seq_offsets is not None:
+        if seq_offsets.dim() != 1 or seq_offsets.shape[0] < 2:
+            raise ValueError("seq_offsets holds the sequences' starts and the last one's end")
+        n_seq = seq_offsets.shape[0] - 1
+        _tensor("seq_offsets", seq_offsets, torch.int32, (n_seq + 1,), dev)
+    if token_mask is not None:
+        _tensor("token_mask", token_mask, (torch.uint8, torch.bool), (T,), dev)
+    return T, E, topk_ids.shape[1] - n_shared, n_seq
+
+
+def balance_loss(logits, topk_ids, scoring="softmax", seq_offsets=None, token_mask=None, n_shared=0):
+    """moe_balance_loss -> (losses float32 [2]: balance and z loss, counts
+    int32 [S, E], probs float32 [S, E], tokens int32 [S + 2]).
+
+    ``seq_offsets`` int32 [S + 1] on the GPU cuts the rows into sequences
+    (default: all rows are one); ``token_mask`` uint8 or bool [T] leaves out
+    the rows where it is 0.  counts and tokens go to route_grad."""
+    T, E, k, S = _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask)
+    dev = logits.device
+    losses = torch.empty(2, dtype=torch.float32, device=dev)
+    counts = torch.empty((S, E), dtype=torch.int32, device=dev)
+    probs = torch.empty((S, E), dtype=torch.float32, device=dev)
+    tokens = torch.empty(S + 2, dtype=torch.int32, device=dev)
+    need = lib().moe_balance_loss_workspace_size(T, E, S)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call("moe_balance_loss", dev, logits.data_ptr(), topk_ids.data_ptr(), _ptr(token_mask), _ptr(seq_offsets), T, E, k,
+          n_shared, S, SCORING[scoring], losses.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(),
+          ws.data_ptr(), need)
+    return losses, counts, probs, tokens
+
+
+def route_grad(logits, topk_ids, scoring="softmax", renormalize=True, routed_scale=1.0, d_weights=None, d_losses=None,
+               counts=None, tokens=None, seq_offsets=None, token_mask=None, n_shared=0, d_logits=None):
+    """moe_route_grad -> d_logits float32 [T, E], from ``d_weights`` (float32
+    [T, k], the gradient of the routing weights) and / or ``d_losses``
+    (float32 [2] on the GPU, the gradient of balance_loss's losses, with its
+    counts and tokens)."""
+    T, E, k, S = _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask)
+    dev = logits.device
+    if d_weights is None and d_losses is None:
+        raise ValueError("route_grad takes d_weights, d_losses or both")
+    if d_weights is not None:
+        _tensor("d_weights", d_weights, torch.float32, (T, k + n_shared), dev)
+    if d_losses is not None:
+        if counts is None or tokens is None:
+            raise ValueError("d_losses goes with balance_loss's counts and tokens")
+        _tensor("d_losses", d_losses, torch.float32, (2,), dev)
+        _tensor("counts", counts, torch.int32, (S, E), dev)
+        _tensor("tokens", tokens, torch.int32, (S + 2,), dev)
+    if d_logits is None:
+        d_logits = torch.empty_like(logits)
+    else:
+        _tensor("d_logits", d_logits, torch.float32, (T, E), dev)
+    _call("moe_route_grad", dev, logits.data_ptr(), topk_ids.data_ptr(), _ptr(token_mask), _ptr(seq_offsets), T, E, k,
+          n_shared, S, SCORING[scoring], int(bool(renormalize)), routed_scale, _ptr(d_weights), _ptr(d_losses),
+          _ptr(counts), _ptr(tokens), d_logits.data_ptr())
+    return d_logits
+
+
+def gate_grad(x, gate, d_logits, dx_in=None, dx=None, with_dx=True, with_gate=True):
+    """moe_gate_grad -> (dx bf16 [T, H], d_gate float32 [E, H]): dx =
+    d_logits gate (+ dx_in), d_gate = d_logits^T x; None for the one that
+    is not wanted.  dx may be dx_in (in place)."""
+    if x.dim() != 2 or gate.dim() != 2:
+        raise ValueError("x is [T, H] and the gate [E, H]")
+    T, H = x.shape
+    E = gate.shape[0]
+    dev = x.device
+    _tensor("x", x, torch.bfloat16, (T, H), dev)
+    _tensor("gate", gate, _BF16_FP32, (E, H), dev)
+    _tensor("d_logits", d_logits, torch.float32, (T, E), dev)
+    if not with_dx and (dx is not None or dx_in is not None):
+        raise ValueError("dx and dx_in without with_dx")
+    if dx_in is not None:
+        _tensor("dx_in", dx_in, torch.bfloat16, (T, H), dev)
+    if dx is not None:
+        _tensor("dx", dx, torch.bfloat16, (T, H), dev)
+    elif with_dx:
+        dx = torch.empty_like(x)
+    d_gate = torch.empty((E, H), dtype=torch.float32, device=dev) if with_gate else None
+    need = lib().moe_gate_grad_workspace_size(T, H, E)
+    ws = torch.empty(need, dtype=torch.uint8, device=dev)
+    _call("moe_gate_grad", dev, x.data_ptr(), gate.data_ptr(), _TYPE_IS_FP32[gate.dtype], d_logits.data_ptr(),
+          _ptr(dx_in), T, H, E, _ptr(dx), _ptr(d_gate), ws.data_ptr(), need)
+    return dx, d_gate
+
+
+def norm_layer_workspace_size(T, H, E, F, k, block_m=0, wformat="bf16", n_shared=0):
+    return int(lib().moe_norm_layer_workspace_size(T, H, E, F, k, n_shared, block_m, WFORMAT[wformat]))
+
+
+def norm_layer(x, norm_weight, gate, bias, w13, w2, k, residual=None, eps=1e-6, scoring="softmax", n_group=1,
+               topk_group=1, renormalize=True, routed_scale=1.0, wformat="bf16", w13_scale=None, w2_scale=None,
+               block_m=0, return_routing=False, ws=None, out=None, h=None, swiglu_limit=math.inf, n_shared=0):
+    """moe_norm_layer -> (y bf16 [T, H], h) (and topk ids / weights with
+    return_routing): the layer on the norm of x + residual; h is that sum in
+    the residual's type (None without one).  Other arguments as layer."""
+    _check_cuda(x, gate, bias, w13, w2, w13_scale, w2_scale, out, ws)
+    T, H, Ew, F = _dims(x, w13, w2, wformat)
+    E = gate.shape[0]
+    dev = x.device
+    if Ew != E + n_shared:
+        raise ValueError(f"w13 holds {Ew} experts, the gate {E} and n_shared = {n_shared}")
+    _tensor("x", x, torch.bfloat16, (T, H), dev)
+    _tensor("norm_weight", norm_weight, _BF16_FP32, (H,), dev)
+    rf = 0
+    if residual is not None:
+        _tensor("residual", residual, _BF16_FP32, (T, H), dev)
+        rf = _TYPE_IS_FP32[residual.dtype]
+        if h is None:
+            h = torch.empty_like(residual)
+        else:
+            _tensor("h", h, residual.dtype, (T, H), dev)
+    elif h is not None:
+        raise ValueError("h without a residual is x")
+    if out is not None:
+        _tensor("out", out, torch.bfloat16, (T, H), dev)
+    y = torch.empty((T, H), dtype=torch.bfloat16, device=dev) if out is None else out
+    ids = w = None
+    if return_routing:
+        ids = torch.empty((T, k + n_shared), dtype=torch.int32, device=dev)
+        w = torch.empty((T, k + n_shared), dtype=torch.float32, device=dev)
+    wf = WFORMAT[wformat]
+    need = lib().moe_norm_layer_workspace_size(T, H, E, F, k, n_shared, block_m, wf)
+    ws = workspace(dev, need) if ws is None else ws
+    _call("moe_norm_layer", dev, x.data_ptr(), _ptr(residual), rf, norm_weight.data_ptr(),
+          _TYPE_IS_FP32[norm_weight.dtype], eps, _ptr(gate), _gate_is_fp32(gate), _ptr(bias), wf, _ptr(w13),
+          _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), T, H, E, F, k, n_shared, n_group, topk_group, SCORING[scoring],
+          int(bool(renormalize)), float(routed_scale), block_m, float(swiglu_limit), _ptr(h), _ptr(y), _ptr(ids),
+          _ptr(w), _ptr(ws), ws.numel())
+    return (y, h, ids, w) if return_routing else (y, h)
 
 
 def debug_error(ws):

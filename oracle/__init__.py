@@ -31,9 +31,14 @@ Modules:
   block table, padded length).
 * ``ffn``     - expert weights dequantised exactly, SwiGLU expert, activation
   quantisation (emulate mode), direct and grouped combine, full layer.
+* ``norm``    - the root-mean-square norm with the residual's addition, and
+  its gradient.
+* ``balance`` - the balance and z losses with the per-expert counts, and the
+  gradients from the routing weights and the losses to the logits, the gate
+  and the hidden states.
 
 Parity status of each function is stated in its docstring ("pinned by ..."
 or "parity unpinned").
 """
 
-from . import formats, router, align, ffn  # noqa: F401
+from . import formats, router, align, ffn, norm, balance  # noqa: F401
