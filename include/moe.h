@@ -474,8 +474,9 @@ size_t moe_norm_layer_workspace_size(int T, int H, int E, int F, int k, int n_sh
  *  tokens       out, int32 [n_seq + 2]: n_s, then N, then S'
  * A logit of -inf is an expert of score 0; a row of -inf only counts as a
  * token with p = 0 and no z.  A NaN in a row that takes part reaches the
- * losses; rows that do not are not read.  Sums are fp32 in a fixed order
- * (fp64 over sequences).
+ * losses; what other rows hold reaches nothing.  Sums are fp32 in a fixed
+ * order (fp64 over sequences).  A batch of one sequence with T <= 256 and
+ * E <= 256 needs no workspace (the query says 0).
  * Constraints: 0 <= T <= 2^24, 1 <= k <= E <= 1024, k + n_shared <= 16,
  * n_shared in {0, 1}, 1 <= n_seq <= 2^20.
  * ------------------------------------------------------------------------ */

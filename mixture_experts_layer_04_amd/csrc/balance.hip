@@ -17,7 +17,7 @@
 //   both:       d += d_z 2/N lse softmax(l)
 //
 // A token's E logits sit in the registers of 16 neighbouring lanes (64 above
-// 512 experts), so the row sums are four DPP steps and a wave holds four
+// 320 experts), so the row sums are four DPP steps and a wave holds four
 // tokens.  The column sums of the loss are accumulated per lane over the
 // tokens of a run, then added across lanes, waves and runs in a fixed order;
 // only integer counts use atomics, so every result is the same in every run.
@@ -63,17 +63,51 @@ __device__ __forceinline__ void load4(const float* row, int e, int E, float* l) 
   }
 }
 
-// Score and its derivative by the logit (sigmoid and sqrt(softplus)).  With
-// t = exp(-|l|) <= 1 nothing overflows, and 1 - sigmoid is not formed by a
-// subtraction.
-template <int SC>
-__device__ __forceinline__ float score(float l) {
-  const float t = expf(-fabsf(l));
-  if (SC == MOE_SIGMOID) return (l >= 0.f ? 1.f : t) / (1.f + t);
-  return sqrtf(fmaxf(l, 0.f) + log1pf(t));
+// exp2, log2, 1 / x and sqrt are the hardware's (about 1 ulp each); the
+// exponent l log2(e) - m log2(e) is one fma.
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+__device__ __forceinline__ float exp2_(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float rcp_(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// log(1 + x) for x >= 0: the rounding of 1 + x is put back where it counts
+// (below x = 1; above, it is within 1 ulp of the logarithm)
+__device__ __forceinline__ float log1p_(float x) {
+  const float w = 1.f + x;
+  return __builtin_amdgcn_logf(w) * kLn2 + (x < 1.f ? x - (w - 1.f) : 0.f);
+}
+
+// The scores of a row from a = exp(l - m), m its largest logit, which the
+// softmax and the z loss need anyway: with c = exp(-m), sigmoid(l) = a /
+// (a + c), its complement c / (a + c) and exp(l) = a / c, one exponential
+// for all.  Holds while c neither overflows nor vanishes, |m| <= 60 (scores
+// below exp(m - 87) become 0); other rows take the functions of l itself,
+// with t = exp(-|l|) <= 1.
+constexpr float kSafeMax = 60.f;
+struct RowScale {
+  float c, ec;  // exp(-m), exp(m)
+  bool safe;
+};
+__device__ __forceinline__ RowScale row_scale(float m) {
+  return RowScale{exp2_(-m * kLog2e), exp2_(m * kLog2e), fabsf(m) <= kSafeMax};
 }
 template <int SC>
-__device__ __forceinline__ float score_and_slope(float l, float& slope) {
+__device__ __forceinline__ float score(float a, const RowScale& r) {
+  if (SC == MOE_SIGMOID) return a * rcp_(a + r.c);
+  return __builtin_amdgcn_sqrtf(log1p_(a * r.ec));
+}
+template <int SC>
+__device__ __forceinline__ float score_and_slope(float a, const RowScale& r, float& slope) {
+  const float q = rcp_(a + r.c), sig = a * q;
+  if (SC == MOE_SIGMOID) {
+    slope = sig * (r.c * q);
+    return sig;
+  }
+  const float s = __builtin_amdgcn_sqrtf(log1p_(a * r.ec));
+  slope = s > 0.f ? sig * 0.5f * rcp_(s) : 0.f;
+  return s;
+}
+template <int SC>
+__device__ __forceinline__ float far_score_and_slope(float l, float& slope) {
   const float t = expf(-fabsf(l)), r = 1.f / (1.f + t);
   if (SC == MOE_SIGMOID) {
     slope = t * r * r;
@@ -127,65 +161,94 @@ struct BalanceP {
 };
 
 // One workgroup per chunk of rows: the pieces of the sequences in it.
-template <int LANES, int NV, int SC>
-__global__ __launch_bounds__(256) void balance_kernel(BalanceP p) {
-  constexpr int V = 4 * NV, GROUPS = 256 / LANES;
-  extern __shared__ float lds[];  // [4][Ep] column sums per wave, then [Ep] counts
-  int32_t* hist = reinterpret_cast<int32_t*>(lds + 4 * p.Ep);
-  __shared__ float zw[4];
-  __shared__ int nw[4];
+// Token t's logits, its slots' ids and its mask are on their way while the
+// tokens before it are worked on (logits and ids one token of the lane group
+// ahead, the mask two).
+// ALL: one workgroup for a small batch of one sequence, which writes the
+// results itself (one launch instead of three).
+template <int LANES, int NV, int SC, int NT, bool ALL>
+__global__ __launch_bounds__(NT) void balance_kernel(BalanceP p) {
+  constexpr int V = 4 * NV, GROUPS = NT / LANES, WAVES = NT / kWave;
+  extern __shared__ float lds[];  // [WAVES][Ep] column sums per wave, then [Ep] counts
+  int32_t* hist = reinterpret_cast<int32_t*>(lds + WAVES * p.Ep);
+  __shared__ float zw[WAVES], dw[WAVES];
+  __shared__ int nw[WAVES];
   const int j = threadIdx.x % LANES, g = threadIdx.x / LANES, wave = threadIdx.x >> 6;
   const int a = blockIdx.x * p.chunk, b = min(p.T, a + p.chunk);
   int s = p.off ? seq_of(p.off, p.S, p.T, a) : 0;
   for (; s < p.S; ++s) {
     const int lo = p.off ? max(a, seq_at(p.off, s, p.T)) : a;
     const int hi = p.off ? min(b, seq_at(p.off, s + 1, p.T)) : b;
-    if (lo >= b) break;
-    if (lo >= hi) continue;
-    for (int e = threadIdx.x; e < p.Ep; e += 256) hist[e] = 0;
+    if (!ALL && lo >= b) break;
+    if (!ALL && lo >= hi) continue;
+    for (int e = threadIdx.x; e < p.Ep; e += NT) hist[e] = 0;
     __syncthreads();
-    for (int i = threadIdx.x; i < (hi - lo) * p.k; i += 256) {
-      const int t = lo + i / p.k;
-      if (p.mask && !p.mask[t]) continue;
-      const int id = p.ids[(size_t)t * p.ks + i % p.k];
-      if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
-    }
     float acc[V], z = 0.f;
     int n = 0;
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    auto live = [&](int t) { return t < hi && (!p.mask || p.mask[t]); };
+    float l[V], ln[V];
+    int id = -1, idn = -1;
+    auto load = [&](int t, bool on, float(&to)[V], int& slot) {
+      slot = -1;
+      if (!on) return;
+      if (j < p.k) slot = p.ids[(size_t)t * p.ks + j];
+#pragma unroll
+      for (int v = 0; v < NV; ++v) load4(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, to + 4 * v);
+    };
+    bool on = live(lo + g), next = live(lo + g + GROUPS);
+    load(lo + g, on, l, id);
     for (int t = lo + g; t < hi; t += GROUPS) {
-      if (p.mask && !p.mask[t]) continue;
-      float l[V];
+      load(t + GROUPS, next, ln, idn);
+      const bool after = live(t + 2 * GROUPS);
+      if (on) {
+        if (id >= 0 && id < p.E) atomicAdd(&hist[id], 1);
+        float m = kNegInf;
 #pragma unroll
-      for (int v = 0; v < NV; ++v) load4(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, l + 4 * v);
-      float m = kNegInf;
-#pragma unroll
-      for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
-      m = group_max<LANES>(m);
-      if (m == kNegInf) m = 0.f;  // every logit -inf: the sum below is zero
-      float e[V], es = 0.f;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        e[i] = expf(l[i] - m);
-        es += e[i];
-      }
-      es = group_sum<LANES>(es);
-      float tot = es;
-      if (SC != MOE_SOFTMAX) {
-        tot = 0.f;
+        for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
+        m = group_max<LANES>(m);
+        if (m == kNegInf) m = 0.f;  // every logit -inf: the sum below is zero
+        const float ml = m * kLog2e;
+        float e[V], es = 0.f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          e[i] = score<SC>(l[i]);
-          tot += e[i];
+          e[i] = exp2_(fmaf(l[i], kLog2e, -ml));
+          es += e[i];
         }
-        tot = group_sum<LANES>(tot) + kTiny;
-      }
-      const float inv = tot == 0.f ? 0.f : 1.f / tot, lse = es == 0.f ? 0.f : m + logf(es);
+        es = group_sum<LANES>(es);
+        float tot = es;
+        if (SC != MOE_SOFTMAX) {
+          const RowScale r = row_scale(m);
+          tot = 0.f;
+          if (r.safe) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) acc[i] += e[i] * inv;
-      z += lse * lse;
-      ++n;
+            for (int i = 0; i < V; ++i) {
+              e[i] = score<SC>(e[i], r);
+              tot += e[i];
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+              float slope;
+              e[i] = far_score_and_slope<SC>(l[i], slope);
+              tot += e[i];
+            }
+          }
+          tot = group_sum<LANES>(tot) + kTiny;
+        }
+        const float inv = tot == 0.f ? 0.f : rcp_(tot);
+        const float lse = es == 0.f ? 0.f : (ml + __builtin_amdgcn_logf(es)) * kLn2;
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] = fmaf(e[i], inv, acc[i]);
+        z += lse * lse;
+        ++n;
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) l[i] = ln[i];
+      id = idn;
+      on = next;
+      next = after;
     }
     if (LANES == 16) {  // the wave's four tokens
 #pragma unroll
@@ -200,9 +263,11 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceP p) {
     }
     if ((threadIdx.x & 63) < LANES) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = ((i / 4) * LANES + j) * 4 + i % 4;
-        if (e < p.Ep) lds[wave * p.Ep + e] = acc[i];
+      for (int v = 0; v < NV; ++v) {
+        const int e = (v * LANES + j) * 4;
+        if (e < p.Ep)
+          *reinterpret_cast<f32x4_t*>(lds + wave * p.Ep + e) =
+              f32x4_t{acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3]};
       }
       if (j == 0) {
         zw[wave] = z;
@@ -210,14 +275,47 @@ __global__ __launch_bounds__(256) void balance_kernel(BalanceP p) {
       }
     }
     __syncthreads();
-    const size_t slot = (size_t)blockIdx.x + s;
-    for (int e = threadIdx.x; e < p.Ep; e += 256) {
-      p.psum[slot * p.Ep + e] = (lds[e] + lds[p.Ep + e]) + (lds[2 * p.Ep + e] + lds[3 * p.Ep + e]);
-      p.csum[slot * p.Ep + e] = hist[e];
+    z = 0.f;
+    n = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      z += zw[w];
+      n += nw[w];
     }
-    if (threadIdx.x == 0) {
-      p.zsum[slot] = (zw[0] + zw[1]) + (zw[2] + zw[3]);
-      p.nsum[slot] = nw[0] + nw[1] + nw[2] + nw[3];
+    const size_t slot = (size_t)blockIdx.x + s;
+    float dot = 0.f;
+    for (int e = threadIdx.x; e < p.Ep; e += NT) {
+      float P = 0.f;
+#pragma unroll
+      for (int w = 0; w < WAVES; ++w) P += lds[w * p.Ep + e];
+      const int c = hist[e];
+      if (!ALL) {
+        p.psum[slot * p.Ep + e] = P;
+        p.csum[slot * p.Ep + e] = c;
+      } else if (e < p.E) {
+        P = n > 0 ? P / (float)n : 0.f;
+        p.probs[e] = P;
+        p.counts[e] = c;
+        dot += n > 0 ? (float)c / (float)n * ((float)p.E / (float)p.k) * P : 0.f;
+      }
+    }
+    if (!ALL) {
+      if (threadIdx.x == 0) {
+        p.zsum[slot] = z;
+        p.nsum[slot] = n;
+      }
+    } else {
+      dot = wave_sum(dot);
+      if ((threadIdx.x & 63) == 0) dw[wave] = dot;
+      __syncthreads();
+      if (threadIdx.x == 0) {
+        dot = 0.f;
+        for (int w = 0; w < WAVES; ++w) dot += dw[w];
+        p.losses[0] = dot;
+        p.losses[1] = n > 0 ? z / (float)n : 0.f;
+        p.nseq[0] = p.nseq[1] = n;
+        p.nseq[2] = n > 0;
+      }
     }
     __syncthreads();
   }
@@ -340,9 +438,30 @@ struct RouteGradP {
   const int32_t* tokens;
   float* out;
   int T, E, k, ks, S, renorm;
+  int rows;  // tokens per workgroup
   float scale;
 };
 
+// Value of lane i of the caller's group (i uniform).
+template <int LANES, int I>
+__device__ __forceinline__ int group_bcast(int v) {
+  if (LANES == 16) return __builtin_amdgcn_update_dpp(v, v, 0x150 + I, 0xF, 0xF, false);  // row_newbcast
+  return __builtin_amdgcn_readlane(v, I);
+}
+// sum over the slots i < k that hold this lane's id, of their values, in order
+template <int LANES, int I>
+__device__ __forceinline__ float same_id_sum(int id, float v, int k, float sum) {
+  if (I < k) {
+    const int oid = group_bcast<LANES, I>(id);
+    const float ov = __builtin_bit_cast(float, group_bcast<LANES, I>(__builtin_bit_cast(int, v)));
+    sum += oid == id ? ov : 0.f;
+    if constexpr (I + 1 < 16) return same_id_sum<LANES, I + 1>(id, v, k, sum);
+  }
+  return sum;
+}
+
+// One workgroup per run of `rows` tokens; a lane group takes every GROUPS-th
+// of them, with the next one's logits and slots on their way.
 template <int LANES, int NV, int SC>
 __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradP p) {
   constexpr int V = 4 * NV, GROUPS = 256 / LANES, ROW = NV * LANES * 4;
@@ -351,81 +470,121 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradP p) {
   float* gwrow = gwbuf + g * ROW;
 #pragma unroll
   for (int v = 0; v < NV; ++v) *reinterpret_cast<f32x4_t*>(gwrow + (v * LANES + j) * 4) = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  const float da = p.d_losses ? p.d_losses[0] : 0.f, dz = p.d_losses ? p.d_losses[1] : 0.f;
-  const float total = p.d_losses ? (float)p.tokens[p.S] : 1.f, full = p.d_losses ? (float)p.tokens[p.S + 1] : 1.f;
-  for (int t0 = blockIdx.x * GROUPS; t0 < p.T; t0 += gridDim.x * GROUPS) {
-    const int t = t0 + g;
-    if (t >= p.T) continue;
-    // the losses' part: rows of a sequence that the mask keeps
-    bool loss = p.d_losses != nullptr && !(p.mask && !p.mask[t]);
-    int s = 0;
+  const int a = blockIdx.x * p.rows, b = min(p.T, a + p.rows);
+  const bool losses = p.d_losses != nullptr, wants = p.d_weights != nullptr;
+  float da = 0.f, dz = 0.f;
+  if (losses) {
+    const float total = (float)p.tokens[p.S], full = (float)p.tokens[p.S + 1];
+    da = p.d_losses[0] * ((float)p.E / (float)p.k) / full;
+    dz = p.d_losses[1] * 2.f / total;
+  }
+  // the sequence of the group's token, its rows [lo, hi) and its gradient to
+  // the probabilities, kept while the tokens stay in it
+  int s = losses && p.off ? seq_of(p.off, p.S, p.T, a) : 0, lo = 0, hi = p.T;
+  if (losses && p.off) {
+    lo = seq_at(p.off, s, p.T);
+    hi = seq_at(p.off, s + 1, p.T);
+  }
+  int have = -1;
+  float gb[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) gb[i] = 0.f;
+
+  float l[V], ln[V];
+  int id = -1, idn = -1;
+  float dw = 0.f, dwn = 0.f;
+  bool on = false, onn = false;
+  auto load = [&](int t, float(&to)[V], int& slot, float& w, bool& keep) {
+    slot = -1;
+    w = 0.f;
+    keep = false;
+    if (t >= b) return;
+    keep = !p.mask || p.mask[t];
+    if (wants && j < p.k) {
+      slot = p.ids[(size_t)t * p.ks + j];
+      w = p.d_weights[(size_t)t * p.ks + j];
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) load4(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, to + 4 * v);
+  };
+  load(a + g, l, id, dw, on);
+  for (int t = a + g; t < b; t += GROUPS) {
+    load(t + GROUPS, ln, idn, dwn, onn);
+    const float* row = p.logits + (size_t)t * p.E;
+    if (id < 0 || id >= p.E) {
+      id = -1;
+      dw = 0.f;
+    }
+    const float lsel = id >= 0 ? row[id] : 0.f;
+    dw *= p.scale;
+    const bool weights = wants && group_max<LANES>(dw != 0.f ? 1.f : 0.f) > 0.f;  // NaN counts
+    bool loss = losses && on;
     if (loss && p.off) {
-      s = seq_of(p.off, p.S, p.T, t);
-      loss = seq_at(p.off, s, p.T) <= t && t < seq_at(p.off, s + 1, p.T);
+      while (t >= hi && s + 1 < p.S) {
+        ++s;
+        lo = hi;
+        hi = seq_at(p.off, s + 1, p.T);
+      }
+      loss = lo <= t && t < hi;
     }
-    // the weights' part: slot j of the token on lane j
-    int id = -1;
-    float dw = 0.f;
-    if (p.d_weights && j < p.k) {
-      id = p.ids[(size_t)t * p.ks + j];
-      if (id < 0 || id >= p.E)
-        id = -1;
-      else
-        dw = p.d_weights[(size_t)t * p.ks + j] * p.scale;
-    }
-    const bool weights = group_max<LANES>(dw != 0.f ? 1.f : 0.f) > 0.f;  // NaN counts
-    float* out = p.out + (size_t)t * p.E;
     float d[V];
     if (!loss && !weights) {
 #pragma unroll
       for (int i = 0; i < V; ++i) d[i] = 0.f;
     } else {
-      const float* row = p.logits + (size_t)t * p.E;
-      float l[V];
-#pragma unroll
-      for (int v = 0; v < NV; ++v) load4(row, (v * LANES + j) * 4, p.E, l + 4 * v);
       float m = kNegInf;
 #pragma unroll
       for (int i = 0; i < V; ++i) m = fmaxf(m, l[i]);
       m = group_max<LANES>(m);
       if (m == kNegInf) m = 0.f;
+      const float ml = m * kLog2e;
       float soft[V], es = 0.f;
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        soft[i] = expf(l[i] - m);
+        soft[i] = exp2_(fmaf(l[i], kLog2e, -ml));
         es += soft[i];
       }
       es = group_sum<LANES>(es);
-      const float einv = es == 0.f ? 0.f : 1.f / es, lse = es == 0.f ? 0.f : m + logf(es);
+      const float einv = es == 0.f ? 0.f : rcp_(es);
+      const float beta = loss && es != 0.f ? dz * (ml + __builtin_amdgcn_logf(es)) * kLn2 : 0.f;
+      float sel = id >= 0 ? exp2_(fmaf(lsel, kLog2e, -ml)) : 0.f;
+      float sc[V], slope[V], tinv = 1.f;
+      if (SC == MOE_SOFTMAX) {
+        sel *= einv;
 #pragma unroll
-      for (int i = 0; i < V; ++i) soft[i] *= einv;
-      float sc[V], slope[V], tot = 0.f;
-      if (SC != MOE_SOFTMAX) {
+        for (int i = 0; i < V; ++i) soft[i] *= einv;
+      } else {
+        const RowScale r = row_scale(m);
+        float tot = 0.f;
+        if (r.safe) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          sc[i] = score_and_slope<SC>(l[i], slope[i]);
-          tot += sc[i];
+          for (int i = 0; i < V; ++i) {
+            sc[i] = score_and_slope<SC>(soft[i], r, slope[i]);
+            tot += sc[i];
+          }
+          sel = id >= 0 ? score<SC>(sel, r) : 0.f;
+        } else {
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            sc[i] = far_score_and_slope<SC>(l[i], slope[i]);
+            tot += sc[i];
+          }
+          float unused;
+          sel = id >= 0 ? far_score_and_slope<SC>(lsel, unused) : 0.f;
         }
-        tot = group_sum<LANES>(tot) + kTiny;
+        tinv = rcp_(group_sum<LANES>(tot) + kTiny);
       }
       float gw[V];
 #pragma unroll
       for (int i = 0; i < V; ++i) gw[i] = 0.f;
       if (weights) {
-        float sel = 0.f;
-        if (id >= 0) sel = SC == MOE_SOFTMAX ? expf(row[id] - m) * einv : score<SC>(row[id]);
         float ds = dw;
         if (p.renorm) {
-          const float den = group_sum<LANES>(sel) + kTiny;
-          ds = (dw - group_sum<LANES>(id >= 0 ? dw * sel : 0.f) / den) / den;
+          const float inv = rcp_(group_sum<LANES>(sel) + kTiny);
+          ds = (dw - group_sum<LANES>(id >= 0 ? dw * sel : 0.f) * inv) * inv;
         }
         // slots that chose the same expert: each gets the sum of all of them
-        float sum = 0.f;
-        for (int i = 0; i < p.k; ++i) {
-          const int oid = __shfl(id, i, LANES);
-          const float od = __shfl(ds, i, LANES);
-          if (oid == id) sum += od;
-        }
+        const float sum = same_id_sum<LANES, 0>(id, ds, p.k, 0.f);
         if (id >= 0) gwrow[id] = sum;
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
@@ -441,34 +600,46 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradP p) {
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
       }
-      float gb[V], beta = 0.f;
+      if (loss && have != s) {
+        have = s;
+        const float n = (float)p.tokens[s], alpha = da / (n * n);
 #pragma unroll
-      for (int i = 0; i < V; ++i) gb[i] = 0.f;
-      if (loss) {
-        const float n = (float)p.tokens[s];
-        const float alpha = da * ((float)p.E / (float)p.k) / (n * n * full);
-        beta = dz * 2.f / total * lse;
+        for (int v = 0; v < NV; ++v) {
+          const int e = (v * LANES + j) * 4;
+          i32x4_t c = {0, 0, 0, 0};
+          const int32_t* at = p.counts + (size_t)s * p.E + e;
+          if (e + 4 <= p.E) {
+            __builtin_memcpy(&c, at, 16);
+          } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-          const int e = ((i / 4) * LANES + j) * 4 + i % 4;
-          if (e < p.E) gb[i] = alpha * (float)p.counts[(size_t)s * p.E + e];
+            for (int i = 0; i < 4; ++i)
+              if (e + i < p.E) c[i] = at[i];
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i) gb[4 * v + i] = alpha * (float)c[i];
         }
       }
+      const float on_loss = loss ? 1.f : 0.f;
       float dot = 0.f;
       if (SC == MOE_SOFTMAX) {
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot += soft[i] * (gb[i] + gw[i]);
-        dot = group_sum<LANES>(dot);
+        for (int i = 0; i < V; ++i) {
+          gw[i] = fmaf(gb[i], on_loss, gw[i]);
+          dot = fmaf(soft[i], gw[i], dot);
+        }
+        const float shift = beta - group_sum<LANES>(dot);
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = soft[i] * ((gb[i] + gw[i]) - dot + beta);
+        for (int i = 0; i < V; ++i) d[i] = soft[i] * (gw[i] + shift);
       } else {
 #pragma unroll
-        for (int i = 0; i < V; ++i) dot += sc[i] * gb[i];
-        dot = group_sum<LANES>(dot) / tot;
+        for (int i = 0; i < V; ++i) dot = fmaf(sc[i], gb[i], dot);
+        dot = group_sum<LANES>(dot) * tinv;
+        const float scale = tinv * on_loss, zs = beta * einv;
 #pragma unroll
-        for (int i = 0; i < V; ++i) d[i] = slope[i] * ((gb[i] - dot) / tot + gw[i]) + beta * soft[i];
+        for (int i = 0; i < V; ++i) d[i] = slope[i] * fmaf(gb[i] - dot, scale, gw[i]) + zs * soft[i];
       }
     }
+    float* out = p.out + (size_t)t * p.E;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
       const int e = (v * LANES + j) * 4;
@@ -481,6 +652,11 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradP p) {
           if (e + i < p.E) out[e + i] = d[4 * v + i];
       }
     }
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = ln[i];
+    id = idn;
+    dw = dwn;
+    on = onn;
   }
 }
 
@@ -490,6 +666,7 @@ int balance_chunk(int T) { return T <= 16 * 1024 ? 16 : ceil_div(ceil_div(T, 102
 struct BalanceLayout {
   size_t psum, csum, zsum, nsum, dot, zseq, total;
 };
+bool balance_in_one(int T, int E, int S);
 BalanceLayout balance_layout(int T, int E, int S) {
   const size_t Ep = align_up((size_t)E, 64);
   const size_t slots = (size_t)ceil_div(T, balance_chunk(T)) + S;
@@ -500,6 +677,8 @@ BalanceLayout balance_layout(int T, int E, int S) {
     off += align_up(bytes, 256);
     return at;
   };
+  L.total = 0;
+  if (balance_in_one(T, E, S)) return L;  // no scratch memory
   L.psum = take(slots * Ep * 4);
   L.csum = take(slots * Ep * 4);
   L.zsum = take(slots * 4);
@@ -518,19 +697,34 @@ moe_status router_shape(int T, int E, int k, int n_shared, int n_seq, int scorin
   return MOE_OK;
 }
 
+// One workgroup of 16 waves for a small batch of one sequence.
+bool balance_in_one(int T, int E, int S) { return S == 1 && T <= 256 && E <= 256; }
+
+template <int LANES, int NV, int SC>
+void balance_launch_sc(const BalanceP& p, bool one, hipStream_t s) {
+  if constexpr (LANES == 16 && NV <= 4) {
+    if (one) {
+      balance_kernel<LANES, NV, SC, 1024, true><<<1, 1024, (size_t)17 * p.Ep * 4, s>>>(p);
+      return;
+    }
+  }
+  balance_kernel<LANES, NV, SC, 256, false><<<p.chunks, 256, (size_t)5 * p.Ep * 4, s>>>(p);
+}
 template <int LANES, int NV>
-void balance_launch(const BalanceP& p, int scoring, hipStream_t s) {
-  const size_t lds = (size_t)5 * p.Ep * 4;
+void balance_launch(const BalanceP& p, bool one, int scoring, hipStream_t s) {
   switch (scoring) {
-    case MOE_SOFTMAX: balance_kernel<LANES, NV, MOE_SOFTMAX><<<p.chunks, 256, lds, s>>>(p); break;
-    case MOE_SIGMOID: balance_kernel<LANES, NV, MOE_SIGMOID><<<p.chunks, 256, lds, s>>>(p); break;
-    default: balance_kernel<LANES, NV, MOE_SQRTSOFTPLUS><<<p.chunks, 256, lds, s>>>(p); break;
+    case MOE_SOFTMAX: balance_launch_sc<LANES, NV, MOE_SOFTMAX>(p, one, s); break;
+    case MOE_SIGMOID: balance_launch_sc<LANES, NV, MOE_SIGMOID>(p, one, s); break;
+    default: balance_launch_sc<LANES, NV, MOE_SQRTSOFTPLUS>(p, one, s); break;
   }
 }
 template <int LANES, int NV>
-void route_grad_launch(const RouteGradP& p, int scoring, hipStream_t s) {
-  const int64_t need = ceil_div64(p.T, 256 / LANES);
-  const int grid = (int)(need < 4096 ? need : 4096);
+void route_grad_launch(RouteGradP p, int scoring, hipStream_t s) {
+  // one token per lane group until the chip is full, then up to four
+  constexpr int GROUPS = 256 / LANES;
+  const int64_t runs = ceil_div64(p.T, GROUPS);
+  p.rows = GROUPS * (int)(runs <= 1024 ? 1 : runs >= 4096 ? 4 : ceil_div64(runs, 1024));
+  const int grid = ceil_div(p.T, p.rows);
   switch (scoring) {
     case MOE_SOFTMAX: route_grad_kernel<LANES, NV, MOE_SOFTMAX><<<grid, 256, 0, s>>>(p); break;
     case MOE_SIGMOID: route_grad_kernel<LANES, NV, MOE_SIGMOID><<<grid, 256, 0, s>>>(p); break;
@@ -538,20 +732,20 @@ void route_grad_launch(const RouteGradP& p, int scoring, hipStream_t s) {
   }
 }
 
-// 16 lanes per token up to 512 experts (4 per lane and 64 of them), else 64
-#define MOE_BY_EXPERTS(FN, E, ...)                  \
-  do {                                              \
-    switch (ceil_div(E, 64)) {                      \
-      case 1: FN<16, 1>(__VA_ARGS__); break;        \
-      case 2: FN<16, 2>(__VA_ARGS__); break;        \
-      case 3: FN<16, 3>(__VA_ARGS__); break;        \
-      case 4: FN<16, 4>(__VA_ARGS__); break;        \
-      case 5: FN<16, 5>(__VA_ARGS__); break;        \
-      case 6: FN<16, 6>(__VA_ARGS__); break;        \
-      case 7: case 8: FN<16, 8>(__VA_ARGS__); break; \
-      case 9: case 10: case 11: case 12: FN<64, 3>(__VA_ARGS__); break; \
-      default: FN<64, 4>(__VA_ARGS__); break;       \
-    }                                               \
+// 16 lanes per token up to 320 experts (20 logits a lane), else 64: above,
+// the gradient's rows would take more registers than two waves per SIMD have.
+#define MOE_BY_EXPERTS(FN, E, ...)             \
+  do {                                         \
+    switch (ceil_div(E, 64)) {                 \
+      case 1: FN<16, 1>(__VA_ARGS__); break;   \
+      case 2: FN<16, 2>(__VA_ARGS__); break;   \
+      case 3: FN<16, 3>(__VA_ARGS__); break;   \
+      case 4: FN<16, 4>(__VA_ARGS__); break;   \
+      case 5: FN<16, 5>(__VA_ARGS__); break;   \
+      case 6: case 7: case 8: FN<64, 2>(__VA_ARGS__); break;              \
+      case 9: case 10: case 11: case 12: FN<64, 3>(__VA_ARGS__); break;   \
+      default: FN<64, 4>(__VA_ARGS__); break;  \
+    }                                          \
   } while (0)
 
 }  // namespace
@@ -572,8 +766,9 @@ extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_
   if (st != MOE_OK) return st;
   if (!seq_offsets && n_seq != 1) return MOE_E_INVAL;
   if (T > 0 && (!logits || !topk_ids)) return MOE_E_INVAL;
-  if (!losses || !counts || !probs || !tokens || !workspace) return MOE_E_INVAL;
+  if (!losses || !counts || !probs || !tokens) return MOE_E_INVAL;
   const BalanceLayout L = balance_layout(T, E, n_seq);
+  if (L.total > 0 && !workspace) return MOE_E_INVAL;
   if (workspace_bytes < L.total) return MOE_E_WORKSPACE;
   char* b = static_cast<char*>(workspace);
   BalanceP p;
@@ -599,10 +794,16 @@ extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_
   p.losses = losses;
   p.counts = counts;
   p.probs = probs;
-  if (T > 0) {
-    MOE_BY_EXPERTS(balance_launch, E, p, scoring, stream);
+  const bool one = balance_in_one(T, E, n_seq);
+  if (one) {
+    p.chunk = T > 0 ? T : 1;
+    p.chunks = 1;
+  }
+  if (T > 0 || one) {
+    MOE_BY_EXPERTS(balance_launch, E, p, one, scoring, stream);
     MOE_CHECK_LAUNCH();
   }
+  if (one) return MOE_OK;
   const dim3 grid((unsigned)n_seq, (unsigned)(p.Ep / 64));
   balance_seq_kernel<<<grid, 1024, 0, stream>>>(p);
   MOE_CHECK_LAUNCH();

@@ -56,7 +56,8 @@ def test_balance_loss(L):
     assert call(k=33) == INVAL and call(k=17) == INVAL and call(k=16, ns=1) == INVAL and call(ns=2) == INVAL
     assert call(S=0) == INVAL and call(S=2) == INVAL and call(off=FAKE, S=(1 << 20) + 1) == INVAL
     assert call(sc=3) == INVAL and call(lg=None) == INVAL and call(ids=None) == INVAL and call(out=None) == INVAL
-    assert call(ws=None) == INVAL and call(n=1000) == WORKSPACE
+    assert call(T=300, ws=None) == INVAL and call(T=300, n=1000) == WORKSPACE
+    assert L.moe_balance_loss_workspace_size(256, 256, 1) == 0  # one launch, no scratch memory
     assert L.moe_balance_loss_workspace_size(-1, 8, 1) == 0 and L.moe_balance_loss_workspace_size(8, 8, 0) == 0
     small, large = (L.moe_balance_loss_workspace_size(T, 256, 4) for T in (16, 100000))
     assert 65536 < small < large
