@@ -20,6 +20,8 @@
 // row l % 16, K values 8 (l / 16) .. + 7 at byte 16 l.  A fragment is then
 // one contiguous copy into LDS and one conflict-free 16-byte read per lane.
 
+#include <utility>
+
 #include "common.h"
 #include "launch.h"
 
@@ -28,15 +30,57 @@ namespace moe {
 namespace {
 
 constexpr int kFrag = 512;  // bf16 values of a fragment (1 KiB)
-constexpr int kMaxMf = 4;   // 16-row fragments of experts per wave of the d_gate kernel
+constexpr int kMaxMf = 4;   // 16-expert fragments per wave of the d_gate kernel
 
-typedef __attribute__((address_space(1))) void gmem_t;
-typedef __attribute__((address_space(3))) void lmem_t;
+typedef __amdgpu_buffer_rsrc_t rsrc_t;
+typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 
-// 64 lanes x 16 contiguous bytes from g + 16 lane to the wave-uniform LDS
-// address + 16 lane
-__device__ __forceinline__ void copy_frag(const uint16_t* g, uint16_t* lds, int lane) {
-  __builtin_amdgcn_global_load_lds((gmem_t*)(g + lane * 8), (lmem_t*)lds, 16, 0, 0);
+// Buffer range at `base`: loads at or past its end give zero, stores there
+// are dropped, and either way the instruction is issued (the waits below
+// count instructions).
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint64_t bytes) {
+  const uint32_t n = bytes > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)bytes;
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)n, 0x00020000);
+}
+// The same range as the four words of a descriptor, in scalar registers.
+__device__ __forceinline__ i32x4_t make_desc(const void* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)base;
+  return i32x4_t{__builtin_amdgcn_readfirstlane((int)(uint32_t)b),
+                 __builtin_amdgcn_readfirstlane((int)((uint32_t)(b >> 32) & 0xFFFFu)),
+                 __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000};
+}
+__device__ __forceinline__ uint32_t lds_addr(const void* p) {
+  return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
+}
+// Copy of 16 bytes per lane from byte voff + soff of the range to LDS address
+// dst + 16 lane (copy_frag: 64 lanes x 16 contiguous bytes).  Written as assembly (it has no result
+// register) because the compiler puts a wait for every copy that it knows of
+// ahead of LDS reads it cannot tell from the copy's target, which here would
+// be a wait for the whole pipeline in each step; the waits below are the
+// ones that are needed.  The s_nop is the wait state between a write of m0
+// and its use.
+__device__ __forceinline__ void copy16(const i32x4_t& r, uint32_t voff, uint32_t soff, uint32_t dst) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+                   __builtin_amdgcn_readfirstlane(dst)),
+               "v"(voff), "s"(r), "s"(__builtin_amdgcn_readfirstlane(soff))
+               : "memory", "m0");
+}
+__device__ __forceinline__ void copy_frag(const i32x4_t& r, uint32_t soff, uint32_t dst, int lane) {
+  copy16(r, lane * 16, soff, dst);
+}
+template <int N>
+__device__ __forceinline__ void wait_vm() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N < 63 ? N : 63) : "memory");
+}
+// Memory operations stay on their side of it.
+__device__ __forceinline__ void keep_order() { asm volatile("" ::: "memory"); }
+// Barrier that waits for this wave's LDS operations but leaves its vector
+// memory operations in flight; what others need of those, the wave has
+// waited for before it.
+__device__ __forceinline__ void step_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
 }
 
 // v = hi + mid + lo, each a bf16 (the upper 16 bits of an fp32); a value that
@@ -64,14 +108,16 @@ struct GateGradP {
   uint16_t* dx;
   float* d_gate;
   int T, H, E, gate_fp32;
-  int Kf;       // K fragments of dx: E / 32 rounded up
+  int Kf;       // K fragments of dx: E / 32 rounded up (to one of the kernel's counts)
+  int mt;       // 16-token fragments per wave of dx: 2, 1, or 0 for the kernel of many experts
+  int hsplits, hper;  // column splits of dx, 64-column blocks of each
   int tiles_t;  // 128-token tiles
   int nt32;     // K steps of d_gate: T / 32 rounded up
   int Ef;       // 16-expert fragments of d_gate, all M tiles
-  int mtiles, mf;  // M tiles of d_gate, of 4 mf fragments each
+  int mtiles, mf;  // M tiles of d_gate, of 2 mf fragments each
   int splits, steps;  // K splits of d_gate, steps of each
   uint16_t* dxa;  // [tiles_t][Kf][2][8][kFrag]   d_logits, rows t
-  uint16_t* dxb;  // [H / 128][Kf][1 or 2][8][kFrag]  gate, rows h
+  uint16_t* dxb;  // [H / 64][Kf][1 or 2][4][kFrag]  gate, rows h
   uint16_t* dga;  // [nt32][3][Ef][kFrag]  d_logits, rows e
   float* part;    // [splits][E][H]
 };
@@ -141,11 +187,11 @@ __global__ __launch_bounds__(256) void split_gate_kernel(GateGradP p) {
   for (int i = 0; i < 8; ++i) split3(tile[eg * 8 + i][c], a[i], m[i], l[i]);
   const int planes = p.gate_fp32 ? 2 : 1, lane = h % 16 + 16 * eg;
   uint16_t* at =
-      p.dxb + (((size_t)(h / 128) * p.Kf + blockIdx.x) * planes * 8 + (h % 128) / 16) * kFrag + lane * 8;
+      p.dxb + (((size_t)(h / 64) * p.Kf + blockIdx.x) * planes * 4 + (h % 64) / 16) * kFrag + lane * 8;
   *reinterpret_cast<u32x4_t*>(at) =
       u32x4_t{a[0] | (a[1] << 16), a[2] | (a[3] << 16), a[4] | (a[5] << 16), a[6] | (a[7] << 16)};
   if (planes == 2)
-    *reinterpret_cast<u32x4_t*>(at + 8 * kFrag) =
+    *reinterpret_cast<u32x4_t*>(at + 4 * kFrag) =
         u32x4_t{m[0] | (m[1] << 16), m[2] | (m[3] << 16), m[4] | (m[5] << 16), m[6] | (m[7] << 16)};
 }
 
@@ -153,25 +199,171 @@ __device__ __forceinline__ bf16x8_t frag(const uint16_t* lds, int lane) {
   return *reinterpret_cast<const bf16x8_t*>(lds + lane * 8);
 }
 
-// dx: 128 columns x 128 tokens per workgroup, 2 x 2 waves of 64 x 64.  The
-// gate is the MFMA's row operand, so a lane holds 4 consecutive columns of a
-// token.  GP planes of the gate.
+// Operations that a wave has issued after a ring stage's copy when it waits
+// for the stage ahead of step i of a block of KF steps: the copies of the
+// D - 2 stages behind it, and for every first step (last step) since then the
+// block's n_in copies (n_st stores).  Vector memory operations complete in
+// issue order, so leaving that many in flight means that the stage has
+// landed.
+constexpr int in_flight(int i, int D, int KF, int n_in, int n_st) {
+  int n = D - 2;
+  for (int q = i - D + 1; q <= i - 1; ++q) {
+    const int m = ((q % KF) + KF) % KF;
+    if (m == 0) n += n_in;
+    if (m == KF - 1) n += n_st;
+  }
+  return n;
+}
+
+// dx up to 512 experts: a wave keeps both planes of its 16 MT tokens in
+// registers (all KF steps of them) and the workgroup, 8 waves of different
+// tokens, streams the gate's planes through an LDS ring: per 64 columns, KF
+// stages of 4 GP fragments, in memory order.  The gate is the MFMA's row
+// operand, so a lane holds 4 consecutive columns of a token.  A stage is
+// asked for D - 1 steps ahead.  dx_in comes through LDS too, each wave's rows
+// for itself, one block of 64 columns ahead; the 16-byte pieces of row r are
+// stored XORed with r % 8, so that the 16 rows which a read touches lie in
+// different banks.
+// Workgroups of one column range run on the same XCD (blockIdx % 8 where
+// there are 8 ranges), whose L2 then holds that part of the gate.
+template <int KF, int MT, int GP, bool ADD>
+__global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
+  constexpr int D = 8, SF = 4 * GP;
+  constexpr int N_IN = ADD ? 2 * MT : 0, N_ST = 4 * MT;
+  __shared__ __align__(16) uint16_t ring[D][SF * kFrag];
+  __shared__ __align__(16) uint16_t adds[ADD ? 2 : 1][ADD ? 8 * MT * 16 * 64 : 8];  // [block][token][64 columns]
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int hs = blockIdx.x % p.hsplits, tg = blockIdx.x / p.hsplits;
+  const int hb0 = hs * p.hper, hb1 = min(p.H / 64, hb0 + p.hper);
+  const int total = (hb1 - hb0) * KF;  // >= 1
+  const i32x4_t gb = make_desc(p.dxb + (size_t)hb0 * KF * SF * kFrag, (uint32_t)total * SF * kFrag * 2);
+  auto copy = [&](int s) {  // past the end: the last stage again, into a slot nobody reads
+    if (SF == 8 || wave < SF)
+      copy_frag(gb, (uint32_t)((min(s, total - 1) * SF + wave) * kFrag * 2), lds_addr(ring[s % D] + wave * kFrag), lane);
+  };
+  bf16x8_t th[MT][KF], tm[MT][KF];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int tf = min((tg * 8 + wave) * MT + m, p.tiles_t * 8 - 1);
+    const uint16_t* at = p.dxa + ((size_t)(tf / 8) * KF * 16 + tf % 8) * kFrag + lane * 8;
+#pragma unroll
+    for (int k = 0; k < KF; ++k) {
+      th[m][k] = *reinterpret_cast<const bf16x8_t*>(at + (size_t)k * 16 * kFrag);
+      tm[m][k] = *reinterpret_cast<const bf16x8_t*>(at + (size_t)(k * 16 + 8) * kFrag);
+    }
+  }
+  // this workgroup's rows of dx_in and dx
+  const int t0 = tg * 8 * MT * 16;
+  const uint64_t rows = t0 < p.T ? (uint64_t)min(p.T - t0, 8 * MT * 16) : 0;
+  const size_t origin = (size_t)t0 * p.H;
+  const i32x4_t in = make_desc(ADD ? p.dx_in + origin : nullptr, (uint32_t)(rows * p.H * 2));
+  uint32_t add_at[2 * MT];  // 8 rows of 128 bytes per copy
+#pragma unroll
+  for (int c = 0; c < 2 * MT; ++c)
+    add_at[c] = ((wave * MT) * 16 + c * 8 + lane / 8) * (uint32_t)p.H * 2 + ((lane % 8) ^ (lane / 8)) * 16;
+  auto copy_add = [&](int hb) {  // past the end: the last block again
+#pragma unroll
+    for (int c = 0; c < 2 * MT; ++c)
+      copy16(in, add_at[c], (uint32_t)min(hb, hb1 - 1) * 128,
+             lds_addr(adds[hb & 1] + (wave * MT * 16 + c * 8) * 64));
+  };
+  const rsrc_t out = make_rsrc(p.dx + origin, rows * p.H * 2);
+  uint32_t at[MT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m) at[m] = ((wave * MT + m) * 16 + lane % 16) * (uint32_t)p.H * 2 + 8 * (lane / 16);
+  if (ADD) copy_add(hb0);
+#pragma unroll
+  for (int s = 0; s < D - 1; ++s) copy(s);
+  int done = 0;  // steps
+  auto block = [&](int hb) {
+    f32x4_t acc[4][MT];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) acc[i][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    const uint32_t col = (uint32_t)hb * 128;
+    auto step = [&](auto tag) {
+      constexpr int k = decltype(tag)::value;
+      // the first stages have fewer operations behind them
+      if (done < D)
+        wait_vm<D - 2>();
+      else
+        wait_vm<in_flight(k, D, KF, N_IN, N_ST)>();
+      step_barrier();  // the stage is there for every wave; the slot of the step before is read
+      copy(done + D - 1);
+      if (ADD && k == 0) copy_add(hb + 1);
+      const uint16_t* B = ring[done % D];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bf16x8_t gh = frag(B + i * kFrag, lane);
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          acc[i][m] = mfma_16x16x32_bf16(gh, th[m][k], acc[i][m]);
+          acc[i][m] = mfma_16x16x32_bf16(gh, tm[m][k], acc[i][m]);
+        }
+        if (GP == 2) {
+          const bf16x8_t gm = frag(B + (4 + i) * kFrag, lane);
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[i][m] = mfma_16x16x32_bf16(gm, th[m][k], acc[i][m]);
+        }
+      }
+      ++done;
+    };
+    [&]<int... K>(std::integer_sequence<int, K...>) { (step(std::integral_constant<int, K>{}), ...); }
+    (std::make_integer_sequence<int, KF>{});
+    if (ADD) {
+      // behind this block's dx_in: the block's own KF copies and the next
+      // dx_in, and, from the second block on, what the block before issued
+      // after its first copy (a wave without a fragment of the stages has no
+      // copies among them)
+      const bool rings = SF == 8 || wave < SF;
+      if (hb == hb0)
+        rings ? wait_vm<KF + N_IN>() : wait_vm<N_IN>();
+      else
+        rings ? wait_vm<2 * KF - 1 + N_IN + N_ST>() : wait_vm<N_IN + N_ST>();
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x4_t v = acc[i][m];
+        if (ADD) {
+          const int r = (wave * MT + m) * 16 + lane % 16, g = lane / 16;
+          const u32x2_t u = *reinterpret_cast<const u32x2_t*>(adds[hb & 1] + r * 64 + ((2 * i + g / 2) ^ (r % 8)) * 8 +
+                                                               (g & 1) * 4);
+          v += f32x4_t{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
+        }
+        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])}, out, at[m],
+                                              col + i * 32, 0);
+      }
+  };
+  for (int hb = hb0; hb < hb1; ++hb) block(hb);
+  wait_vm<0>();  // no copy into LDS outlives the workgroup
+}
+
+// dx above 512 experts: 128 columns x 128 tokens per workgroup, 2 x 2 waves
+// of 64 x 64, both operands through LDS.  GP planes of the gate.
 template <int GP>
-__global__ __launch_bounds__(256) void dx_kernel(GateGradP p) {
+__global__ __launch_bounds__(256) void dx_wide_kernel(GateGradP p) {
   constexpr int AF = 2 * 8, BF = GP * 8;  // fragments per K step
   __shared__ __align__(16) uint16_t lds[2][(AF + BF) * kFrag];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wh = wave & 1, wt = wave >> 1;
-  const uint16_t* ga = nullptr;
-  const uint16_t* gb = p.dxb + (size_t)blockIdx.x * p.Kf * BF * kFrag;
-  auto copy = [&](int s) {
-    uint16_t* to = lds[s & 1];
-    for (int f = wave; f < AF + BF; f += 4)
-      copy_frag(f < AF ? ga + ((size_t)s * AF + f) * kFrag : gb + ((size_t)s * BF + f - AF) * kFrag, to + f * kFrag,
-                lane);
-  };
+  const uint32_t step_b = GP * 4 * kFrag * 2;  // bytes of a 64-column block's step
+  const i32x4_t gb = make_desc(p.dxb + (size_t)blockIdx.x * 2 * p.Kf * GP * 4 * kFrag, 2u * p.Kf * step_b);
   for (int ty = blockIdx.y; ty < p.tiles_t; ty += gridDim.y) {
-    ga = p.dxa + (size_t)ty * p.Kf * AF * kFrag;
+    const i32x4_t ga = make_desc(p.dxa + (size_t)ty * p.Kf * AF * kFrag, (uint32_t)p.Kf * AF * kFrag * 2);
+    auto copy = [&](int s) {
+      uint16_t* to = lds[s & 1];
+      for (int f = wave; f < AF + BF; f += 4) {
+        const int i = f - AF, blk = (i % 8) / 4;  // gate: plane i / 8, fragment i % 8 of two blocks
+        if (f < AF)
+          copy_frag(ga, (uint32_t)((s * AF + f) * kFrag * 2), lds_addr(to + f * kFrag), lane);
+        else
+          copy_frag(gb, (blk * p.Kf + s) * step_b + (uint32_t)(((i / 8) * 4 + i % 4) * kFrag * 2), lds_addr(to + f * kFrag),
+                    lane);
+      }
+    };
     f32x4_t acc[4][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -179,6 +371,7 @@ __global__ __launch_bounds__(256) void dx_kernel(GateGradP p) {
       for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
     copy(0);
     for (int s = 0; s < p.Kf; ++s) {
+      wait_vm<0>();
       __syncthreads();  // step s has landed; step s - 1 is read
       if (s + 1 < p.Kf) copy(s + 1);
       const uint16_t* A = lds[s & 1];
@@ -224,38 +417,67 @@ __global__ __launch_bounds__(256) void dx_kernel(GateGradP p) {
   }
 }
 
-// d_gate: 64 MF experts x 128 columns per workgroup and K split, 4 x 2 waves
-// of 16 MF x 64.  x comes with its rows along K: a thread loads 8 columns of
-// a token and stores them into the fragments one value at a time.  The 16-byte slot of a
-// fragment is XORed with the fragment's number, so that the 16 threads of a
-// token, which write to 8 fragments, meet different banks.
+// d_gate: 32 MF experts x 256 columns per workgroup and K split, 2 x 4 waves
+// of 16 MF x 64.
+//  * The planes of d_logits (24 KiB a step at MF = 4) are copied into a ring
+//    of three steps, two steps ahead.
+//  * x has its rows along K: a thread loads 4 columns of 4 tokens three steps
+//    ahead into registers, transposes them there and stores 8-byte pieces
+//    (4 tokens of a column) into the step's fragments one step ahead.  The
+//    16-byte slot of a fragment is XORed with the fragment's number, so that
+//    lanes which write the same slot of 8 fragments meet different banks.
+//  * Workgroups of one K split that share columns or planes run on the same
+//    XCD (contiguous runs of (split, column tile, expert tile) per XCD).
 template <int MF>
-__global__ __launch_bounds__(512) void d_gate_kernel(GateGradP p) {
-  constexpr int AF = 3 * 4 * MF;
-  __shared__ __align__(16) uint16_t lds[2][(AF + 8) * kFrag];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int wm = wave & 3, wn = wave >> 2;
-  const int h0 = blockIdx.x * 128, mt = blockIdx.y;
-  const int s0 = blockIdx.z * p.steps, s1 = min(p.nt32, s0 + p.steps);
-  auto copy_a = [&](int s, int buf) {
-    for (int f = wave; f < AF; f += 8) {
-      const int plane = f / (4 * MF), i = f % (4 * MF);
-      copy_frag(p.dga + (((size_t)s * 3 + plane) * p.Ef + mt * 4 * MF + i) * kFrag, lds[buf] + f * kFrag, lane);
+__global__ __launch_bounds__(512, 2) void d_gate_kernel(GateGradP p) {
+  constexpr int AF = 3 * 2 * MF, BF = 16;
+  constexpr int N_X = 4, N_A = AF / 8;  // loads of x, and copies (at least), of a wave and step
+  __shared__ __align__(16) uint16_t alds[3][AF * kFrag];
+  __shared__ __align__(16) uint16_t blds[2][BF * kFrag];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave & 1, wn = wave >> 1;
+  const int ht = (p.H + 255) / 256;
+  const int items = ht * p.mtiles * p.splits, per = (items + 7) / 8;
+  const int item = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  if (blockIdx.x / 8 >= per || item >= items) return;
+  const int mt = item % p.mtiles, hx = item / p.mtiles % ht, z = item / p.mtiles / ht;
+  const int h0 = hx * 256;
+  const int s0 = z * p.steps, n = min(p.nt32, s0 + p.steps) - s0;  // >= 1
+  const uint32_t step_bytes = 3u * p.Ef * kFrag * 2;
+  auto copy_a = [&](int s) {  // past the end: the last step again
+    const i32x4_t r = make_desc(p.dga + (size_t)(s0 + min(s, n - 1)) * 3 * p.Ef * kFrag, step_bytes);
+#pragma unroll
+    for (int f0 = 0; f0 < AF; f0 += 8) {
+      const int f = f0 + wave;
+      if (f0 + 8 <= AF || f < AF)
+        copy_frag(r, (uint32_t)(((f / (2 * MF)) * p.Ef + mt * 2 * MF + f % (2 * MF)) * kFrag * 2),
+                  lds_addr(alds[s % 3] + f * kFrag), lane);
     }
   };
-  const int xt = tid / 16, xh = tid % 16;  // this thread's token and 8 columns of a step
-  auto load_x = [&](int s) {
-    const int t = s * 32 + xt;
-    u32x4_t v = {0u, 0u, 0u, 0u};
-    if (t < p.T) v = *reinterpret_cast<const u32x4_t*>(p.x + (size_t)t * p.H + h0 + xh * 8);
-    return v;
-  };
-  auto store_x = [&](const u32x4_t& v, int buf) {
-    uint16_t* B = lds[buf] + AF * kFrag + (xh / 2) * kFrag;
+  // this thread's 4 tokens and 4 columns of a step
+  const int quad = (wave & 3) * 2 + lane / 32, hq = (wave >> 2) * 32 + lane % 32;
+  const int xcol = min(h0 + hq * 4, p.H - 4);  // (columns past H: of the last tile, not stored)
+  u32x2_t xr[3][4];
+  auto load_x = [&](int s, u32x2_t(&to)[4]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int slot = ((xt / 8) * 16 + (xh & 1) * 8 + i) ^ (xh / 2);
-      B[slot * 8 + xt % 8] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
+    for (int i = 0; i < 4; ++i) {
+      const int t = (s0 + s) * 32 + quad * 4 + i;
+      to[i] = *reinterpret_cast<const u32x2_t*>(p.x + (size_t)min(t, p.T - 1) * p.H + xcol);
+    }
+  };
+  auto store_x = [&](int s, u32x2_t(&v)[4]) {
+    const int t = (s0 + s) * 32 + quad * 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (t + i >= p.T) v[i] = u32x2_t{0u, 0u};
+    uint16_t* B = blds[s & 1] + (hq / 4) * kFrag + (quad & 1) * 4;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
+      const u32x2_t w = {__builtin_amdgcn_perm(v[1][c / 2], v[0][c / 2], sel),
+                         __builtin_amdgcn_perm(v[3][c / 2], v[2][c / 2], sel)};
+      const int slot = ((quad / 2) * 16 + (hq % 4) * 4 + c) ^ (hq / 4);
+      *reinterpret_cast<u32x2_t*>(B + slot * 8) = w;
     }
   };
   f32x4_t acc[MF][4];
@@ -263,18 +485,25 @@ __global__ __launch_bounds__(512) void d_gate_kernel(GateGradP p) {
   for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  u32x4_t xv = {0u, 0u, 0u, 0u};
-  if (s0 < s1) {
-    copy_a(s0, 0);
-    store_x(load_x(s0), 0);
-  }
-  for (int s = s0; s < s1; ++s) {
-    const int buf = (s - s0) & 1;
-    if (s + 1 < s1) xv = load_x(s + 1);
-    __syncthreads();  // step s is in LDS; the other buffer is read
-    if (s + 1 < s1) copy_a(s + 1, buf ^ 1);
-    const uint16_t* A = lds[buf];
-    const uint16_t* B = A + AF * kFrag;
+  // x of step s sits in xr[s % 3]; loads past the last step read its rows again
+  load_x(0, xr[0]);
+  load_x(1, xr[1]);
+  copy_a(0);
+  keep_order();
+  load_x(2, xr[2]);
+  copy_a(1);
+  keep_order();
+  store_x(0, xr[0]);
+  // behind step s's copies: the copies of step s + 1 and the loads of x that
+  // go with them (left out of the last step's count: nobody reads what the
+  // step before it loads, so the compiler may drop those)
+  auto step = [&](int s, u32x2_t(&next)[4], u32x2_t(&free)[4], auto behind) {
+    wait_vm<decltype(behind)::value>();
+    step_barrier();
+    load_x(s + 3, free);
+    copy_a(s + 2);
+    const uint16_t* A = alds[s % 3];
+    const uint16_t* B = blds[s & 1];
     bf16x8_t b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) b[j] = frag(B + (wn * 4 + j) * kFrag, lane ^ (wn * 4 + j));
@@ -282,21 +511,33 @@ __global__ __launch_bounds__(512) void d_gate_kernel(GateGradP p) {
     for (int i = 0; i < MF; ++i)
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
-        const bf16x8_t a = frag(A + (q * 4 * MF + wm * MF + i) * kFrag, lane);
+        const bf16x8_t a = frag(A + (q * 2 * MF + wm * MF + i) * kFrag, lane);
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32_bf16(a, b[j], acc[i][j]);
       }
-    if (s + 1 < s1) store_x(xv, buf ^ 1);
+    store_x(s + 1, next);
+  };
+  int s = 0;
+  for (; s + 3 <= n; s += 3) {
+    step(s, xr[1], xr[0], std::integral_constant<int, N_X + N_A>{});
+    step(s + 1, xr[2], xr[1], std::integral_constant<int, N_X + N_A>{});
+    step(s + 2, xr[0], xr[2], std::integral_constant<int, N_X + N_A>{});
   }
-  float* out = p.splits > 1 ? p.part + (size_t)blockIdx.z * p.E * p.H : p.d_gate;
+  if (s < n) step(s, xr[1], xr[0], std::integral_constant<int, N_X + N_A>{});
+  if (s + 1 < n) step(s + 1, xr[2], xr[1], std::integral_constant<int, N_A>{});
+  wait_vm<0>();  // no copy into LDS outlives the workgroup
+  float* out = p.splits > 1 ? p.part + (size_t)z * p.E * p.H : p.d_gate;
 #pragma unroll
   for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int r = 0; r < 4; ++r) {
-      const int e = (mt * 4 * MF + wm * MF + i) * 16 + 4 * (lane / 16) + r;
+      const int e = (mt * 2 * MF + wm * MF + i) * 16 + 4 * (lane / 16) + r;
       if (e >= p.E) continue;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) out[(size_t)e * p.H + h0 + wn * 64 + j * 16 + lane % 16] = acc[i][j][r];
+      for (int j = 0; j < 4; ++j) {
+        const int h = h0 + wn * 64 + j * 16 + lane % 16;
+        if (h < p.H) out[(size_t)e * p.H + h] = acc[i][j][r];
+      }
     }
 }
 
@@ -327,11 +568,21 @@ GateGradPlan gate_grad_plan(int T, int H, int E) {
   p.Kf = ceil_div(E, 32);
   p.tiles_t = ceil_div(T, 128);
   p.nt32 = ceil_div(T, 32);
-  p.mtiles = ceil_div(E, 64 * kMaxMf);
-  p.mf = ceil_div(ceil_div(E, p.mtiles), 64);
-  p.Ef = p.mtiles * 4 * p.mf;
+  // dx: 32 tokens per wave in registers up to 256 experts, 16 up to 512
+  p.mt = p.Kf <= 8 ? 2 : p.Kf <= 16 ? 1 : 0;
+  if (p.Kf == 7) p.Kf = 8;
+  if (p.mt == 1) p.Kf = p.Kf <= 10 ? p.Kf : p.Kf <= 12 ? 12 : 16;
+  const int blocks = H / 64, groups = ceil_div(T, p.mt == 1 ? 128 : 256);
+  p.hsplits = groups >= 32 ? 8 : ceil_div(256, groups > 0 ? groups : 1);
+  if (p.hsplits > blocks) p.hsplits = blocks;
+  p.hper = ceil_div(blocks, p.hsplits);
+  p.hsplits = ceil_div(blocks, p.hper);
+  // d_gate
+  p.mtiles = ceil_div(E, 32 * kMaxMf);
+  p.mf = ceil_div(ceil_div(E, p.mtiles), 32);
+  p.Ef = p.mtiles * 2 * p.mf;
   // about one workgroup per CU, at least 4 steps each
-  const int tiles = (H / 128) * p.mtiles;
+  const int tiles = ceil_div(H, 256) * p.mtiles;
   int splits = 256 / tiles;
   const int most = ceil_div(p.nt32, 4);
   if (splits > most) splits = most;
@@ -346,11 +597,42 @@ GateGradPlan gate_grad_plan(int T, int H, int E) {
   };
   const size_t fb = (size_t)kFrag * 2;
   L.dxa = take((size_t)p.tiles_t * p.Kf * 16 * fb);
-  L.dxb = take((size_t)(H / 128) * p.Kf * 16 * fb);
+  L.dxb = take((size_t)(H / 64) * p.Kf * 8 * fb);
   L.dga = take((size_t)p.nt32 * 3 * p.Ef * fb);
   L.part = take(p.splits > 1 ? (size_t)p.splits * E * H * sizeof(float) : 0);
   L.total = off;
   return L;
+}
+
+template <int KF, int MT>
+void launch_dx_kf(const GateGradP& p, hipStream_t s) {
+  const int grid = ceil_div(p.T, 128 * MT) * p.hsplits;
+  if (p.gate_fp32) {
+    if (p.dx_in)
+      dx_kernel<KF, MT, 2, true><<<grid, 512, 0, s>>>(p);
+    else
+      dx_kernel<KF, MT, 2, false><<<grid, 512, 0, s>>>(p);
+  } else {
+    if (p.dx_in)
+      dx_kernel<KF, MT, 1, true><<<grid, 512, 0, s>>>(p);
+    else
+      dx_kernel<KF, MT, 1, false><<<grid, 512, 0, s>>>(p);
+  }
+}
+void launch_dx(const GateGradP& p, hipStream_t s) {
+  switch (p.Kf) {
+    case 1: launch_dx_kf<1, 2>(p, s); break;
+    case 2: launch_dx_kf<2, 2>(p, s); break;
+    case 3: launch_dx_kf<3, 2>(p, s); break;
+    case 4: launch_dx_kf<4, 2>(p, s); break;
+    case 5: launch_dx_kf<5, 2>(p, s); break;
+    case 6: launch_dx_kf<6, 2>(p, s); break;
+    case 8: launch_dx_kf<8, 2>(p, s); break;
+    case 9: launch_dx_kf<9, 1>(p, s); break;
+    case 10: launch_dx_kf<10, 1>(p, s); break;
+    case 12: launch_dx_kf<12, 1>(p, s); break;
+    default: launch_dx_kf<16, 1>(p, s); break;
+  }
 }
 
 bool gate_grad_shape(int T, int H, int E) {
@@ -402,15 +684,19 @@ extern "C" moe_status moe_gate_grad(const void* x, const void* gate, int gate_is
   if (dx) {
     split_gate_kernel<<<dim3((unsigned)p.Kf, (unsigned)(H / 64)), 256, 0, stream>>>(p);
     MOE_CHECK_LAUNCH();
-    const dim3 grid((unsigned)(H / 128), (unsigned)(p.tiles_t < 65535 ? p.tiles_t : 65535));
-    if (gate_is_fp32)
-      dx_kernel<2><<<grid, 256, 0, stream>>>(p);
-    else
-      dx_kernel<1><<<grid, 256, 0, stream>>>(p);
+    if (p.mt == 0) {
+      const dim3 grid((unsigned)(H / 128), (unsigned)(p.tiles_t < 65535 ? p.tiles_t : 65535));
+      if (gate_is_fp32)
+        dx_wide_kernel<2><<<grid, 256, 0, stream>>>(p);
+      else
+        dx_wide_kernel<1><<<grid, 256, 0, stream>>>(p);
+    } else {
+      launch_dx(p, stream);
+    }
     MOE_CHECK_LAUNCH();
   }
   if (d_gate) {
-    const dim3 grid((unsigned)(H / 128), (unsigned)p.mtiles, (unsigned)p.splits);
+    const int items = ceil_div(H, 256) * p.mtiles * p.splits, grid = ceil_div(items, 8) * 8;
     switch (p.mf) {
       case 1: d_gate_kernel<1><<<grid, 512, 0, stream>>>(p); break;
       case 2: d_gate_kernel<2><<<grid, 512, 0, stream>>>(p); break;
