@@ -20,6 +20,7 @@
 // row l % 16, K values 8 (l / 16) .. + 7 at byte 16 l.  A fragment is then
 // one contiguous copy into LDS and one conflict-free 16-byte read per lane.
 
+#include <type_traits>
 #include <utility>
 
 #include "common.h"
@@ -199,48 +200,83 @@ __device__ __forceinline__ bf16x8_t frag(const uint16_t* lds, int lane) {
   return *reinterpret_cast<const bf16x8_t*>(lds + lane * 8);
 }
 
-// Operations that a wave has issued after a ring stage's copy when it waits
-// for the stage ahead of step i of a block of KF steps: the copies of the
-// D - 2 stages behind it, and for every first step (last step) since then the
-// block's n_in copies (n_st stores).  Vector memory operations complete in
-// issue order, so leaving that many in flight means that the stage has
-// landed.
-constexpr int in_flight(int i, int D, int KF, int n_in, int n_st) {
-  int n = D - 2;
-  for (int q = i - D + 1; q <= i - 1; ++q) {
-    const int m = ((q % KF) + KF) % KF;
-    if (m == 0) n += n_in;
-    if (m == KF - 1) n += n_st;
-  }
-  return n;
+// Item of a grid of 8 ceil(items / 8) workgroups such that each XCD
+// (workgroups are dealt to the XCDs in turn) has a contiguous run of them;
+// -1: none.
+__device__ __forceinline__ int xcd_item(int items) {
+  const int per = (items + 7) / 8, item = (blockIdx.x % 8) * per + blockIdx.x / 8;
+  return (int)blockIdx.x / 8 < per && item < items ? item : -1;
 }
 
 // dx up to 512 experts: a wave keeps both planes of its 16 MT tokens in
 // registers (all KF steps of them) and the workgroup, 8 waves of different
 // tokens, streams the gate's planes through an LDS ring: per 64 columns, KF
-// stages of 4 GP fragments, in memory order.  The gate is the MFMA's row
-// operand, so a lane holds 4 consecutive columns of a token.  A stage is
-// asked for D - 1 steps ahead.  dx_in comes through LDS too, each wave's rows
-// for itself, one block of 64 columns ahead; the 16-byte pieces of row r are
-// stored XORed with r % 8, so that the 16 rows which a read touches lie in
+// stages of 4 GP fragments, in memory order, asked for D - 1 steps ahead.
+// The gate is the MFMA's row operand, so a lane holds 4 consecutive columns
+// of a token.
+//
+// A wave's vector memory operations complete in issue order, so a wave that
+// waits for the ring waits for everything it issued before: waves 0-3 copy
+// the ring (from the L2) and do nothing else, waves 4-7 move the rows of
+// dx_in and dx (HBM).  dx_in comes into LDS one block of 64 columns ahead;
+// the sums, rounded, replace it there; the waves that brought it store them
+// as whole 128-byte rows during the next block.  The 16-byte pieces of row r
+// are XORed with r % 8, so that the 16 rows which an access touches lie in
 // different banks.
-// Workgroups of one column range run on the same XCD (blockIdx % 8 where
-// there are 8 ranges), whose L2 then holds that part of the gate.
+// Items in (token group, column range) order per XCD: its L2 serves a token
+// group's planes to all column ranges, and a gate stage to the few token
+// groups that run beside each other.
 template <int KF, int MT, int GP, bool ADD>
 __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
-  constexpr int D = 8, SF = 4 * GP;
-  constexpr int N_IN = ADD ? 2 * MT : 0, N_ST = 4 * MT;
+  constexpr int D = 8, SF = 4 * GP, ROWS = 8 * MT * 16;
+  constexpr int RC = ROWS / 4 / 8;  // 1 KiB copies (8 rows) of a row-moving wave and block
   __shared__ __align__(16) uint16_t ring[D][SF * kFrag];
-  __shared__ __align__(16) uint16_t adds[ADD ? 2 : 1][ADD ? 8 * MT * 16 * 64 : 8];  // [block][token][64 columns]
+  __shared__ __align__(16) uint16_t rowbuf[2][ROWS * 64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int hs = blockIdx.x % p.hsplits, tg = blockIdx.x / p.hsplits;
+  const int item = xcd_item((p.T + ROWS - 1) / ROWS * p.hsplits);
+  if (item < 0) return;
+  const int hs = item % p.hsplits, tg = item / p.hsplits;
   const int hb0 = hs * p.hper, hb1 = min(p.H / 64, hb0 + p.hper);
   const int total = (hb1 - hb0) * KF;  // >= 1
   const i32x4_t gb = make_desc(p.dxb + (size_t)hb0 * KF * SF * kFrag, (uint32_t)total * SF * kFrag * 2);
   auto copy = [&](int s) {  // past the end: the last stage again, into a slot nobody reads
-    if (SF == 8 || wave < SF)
-      copy_frag(gb, (uint32_t)((min(s, total - 1) * SF + wave) * kFrag * 2), lds_addr(ring[s % D] + wave * kFrag), lane);
+    if (wave < 4) {
+#pragma unroll
+      for (int i = 0; i < GP; ++i)
+        copy_frag(gb, (uint32_t)((min(s, total - 1) * SF + wave * GP + i) * kFrag * 2),
+                  lds_addr(ring[s % D] + (wave * GP + i) * kFrag), lane);
+    }
   };
+  // the rows that waves 4-7 move: 8 per copy, lane l the 16-byte piece l % 8
+  // (XORed) of row l / 8
+  const int t0 = tg * ROWS, r0 = (wave & 3) * (ROWS / 4);
+  const uint64_t bytes = (uint64_t)min(p.T - t0, ROWS) * p.H * 2;  // of the rows below T
+  const size_t origin = (size_t)t0 * p.H;
+  const i32x4_t in = make_desc(ADD ? p.dx_in + origin : nullptr, (uint32_t)bytes);
+  const rsrc_t out = make_rsrc(p.dx + origin, bytes);
+  uint32_t row_at[RC];
+#pragma unroll
+  for (int c = 0; c < RC; ++c)
+    row_at[c] = (r0 + c * 8 + lane / 8) * (uint32_t)p.H * 2 + ((lane % 8) ^ (lane / 8)) * 16;
+  auto copy_rows = [&](int hb) {  // past the end: the last block again
+    if (ADD && wave >= 4) {
+#pragma unroll
+      for (int c = 0; c < RC; ++c)
+        copy16(in, row_at[c], (uint32_t)min(hb, hb1 - 1) * 128, lds_addr(rowbuf[hb & 1] + (r0 + c * 8) * 64));
+    }
+  };
+  auto store_rows = [&](int hb) {
+    if (wave >= 4) {
+#pragma unroll
+      for (int c = 0; c < RC; ++c) {
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(rowbuf[hb & 1] + (r0 + c * 8) * 64 + lane * 8);
+        __builtin_amdgcn_raw_buffer_store_b128(v, out, row_at[c], (uint32_t)hb * 128, 0);
+      }
+    }
+  };
+  copy_rows(hb0);
+#pragma unroll
+  for (int s = 0; s < D - 1; ++s) copy(s);
   bf16x8_t th[MT][KF], tm[MT][KF];
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
@@ -252,46 +288,31 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
       tm[m][k] = *reinterpret_cast<const bf16x8_t*>(at + (size_t)(k * 16 + 8) * kFrag);
     }
   }
-  // this workgroup's rows of dx_in and dx
-  const int t0 = tg * 8 * MT * 16;
-  const uint64_t rows = t0 < p.T ? (uint64_t)min(p.T - t0, 8 * MT * 16) : 0;
-  const size_t origin = (size_t)t0 * p.H;
-  const i32x4_t in = make_desc(ADD ? p.dx_in + origin : nullptr, (uint32_t)(rows * p.H * 2));
-  uint32_t add_at[2 * MT];  // 8 rows of 128 bytes per copy
-#pragma unroll
-  for (int c = 0; c < 2 * MT; ++c)
-    add_at[c] = ((wave * MT) * 16 + c * 8 + lane / 8) * (uint32_t)p.H * 2 + ((lane % 8) ^ (lane / 8)) * 16;
-  auto copy_add = [&](int hb) {  // past the end: the last block again
-#pragma unroll
-    for (int c = 0; c < 2 * MT; ++c)
-      copy16(in, add_at[c], (uint32_t)min(hb, hb1 - 1) * 128,
-             lds_addr(adds[hb & 1] + (wave * MT * 16 + c * 8) * 64));
-  };
-  const rsrc_t out = make_rsrc(p.dx + origin, rows * p.H * 2);
-  uint32_t at[MT];
-#pragma unroll
-  for (int m = 0; m < MT; ++m) at[m] = ((wave * MT + m) * 16 + lane % 16) * (uint32_t)p.H * 2 + 8 * (lane / 16);
-  if (ADD) copy_add(hb0);
-#pragma unroll
-  for (int s = 0; s < D - 1; ++s) copy(s);
   int done = 0;  // steps
-  auto block = [&](int hb) {
+  for (int hb = hb0; hb < hb1; ++hb) {
     f32x4_t acc[4][MT];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int m = 0; m < MT; ++m) acc[i][m] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-    const uint32_t col = (uint32_t)hb * 128;
     auto step = [&](auto tag) {
       constexpr int k = decltype(tag)::value;
-      // the first stages have fewer operations behind them
-      if (done < D)
-        wait_vm<D - 2>();
-      else
-        wait_vm<in_flight(k, D, KF, N_IN, N_ST)>();
-      step_barrier();  // the stage is there for every wave; the slot of the step before is read
+      // waves 0-3: the stage has landed when only the D - 2 behind it are in
+      // flight.  Waves 4-7, ahead of the block's last barrier: this block's
+      // dx_in has when only the stores and dx_in copies of this block's
+      // first step are (with one step a block, those come after the wait).
+      if (wave < 4)
+        wait_vm<(D - 2) * GP>();
+      else if (ADD && k == KF - 1)
+        hb == hb0 ? wait_vm<KF == 1 ? 0 : RC>() : wait_vm<KF == 1 ? 0 : 2 * RC>();
+      step_barrier();  // all of that is there for every wave; the step before is read
       copy(done + D - 1);
-      if (ADD && k == 0) copy_add(hb + 1);
+      if (k == 0) {
+        if (hb > hb0) store_rows(hb - 1);
+        // their reads of that buffer are done before dx_in comes into it
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        copy_rows(hb + 1);
+      }
       const uint16_t* B = ring[done % D];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -311,33 +332,22 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
     };
     [&]<int... K>(std::integer_sequence<int, K...>) { (step(std::integral_constant<int, K>{}), ...); }
     (std::make_integer_sequence<int, KF>{});
-    if (ADD) {
-      // behind this block's dx_in: the block's own KF copies and the next
-      // dx_in, and, from the second block on, what the block before issued
-      // after its first copy (a wave without a fragment of the stages has no
-      // copies among them)
-      const bool rings = SF == 8 || wave < SF;
-      if (hb == hb0)
-        rings ? wait_vm<KF + N_IN>() : wait_vm<N_IN>();
-      else
-        rings ? wait_vm<2 * KF - 1 + N_IN + N_ST>() : wait_vm<N_IN + N_ST>();
-    }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
         f32x4_t v = acc[i][m];
+        const int r = (wave * MT + m) * 16 + lane % 16, g = lane / 16;
+        u32x2_t* at = reinterpret_cast<u32x2_t*>(rowbuf[hb & 1] + r * 64 + ((2 * i + g / 2) ^ (r % 8)) * 8 + (g & 1) * 4);
         if (ADD) {
-          const int r = (wave * MT + m) * 16 + lane % 16, g = lane / 16;
-          const u32x2_t u = *reinterpret_cast<const u32x2_t*>(adds[hb & 1] + r * 64 + ((2 * i + g / 2) ^ (r % 8)) * 8 +
-                                                               (g & 1) * 4);
+          const u32x2_t u = *at;
           v += f32x4_t{bf16_lo(u[0]), bf16_hi(u[0]), bf16_lo(u[1]), bf16_hi(u[1])};
         }
-        __builtin_amdgcn_raw_buffer_store_b64(u32x2_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])}, out, at[m],
-                                              col + i * 32, 0);
+        *at = u32x2_t{cvt_bf16x2(v[0], v[1]), cvt_bf16x2(v[2], v[3])};
       }
-  };
-  for (int hb = hb0; hb < hb1; ++hb) block(hb);
+  }
+  step_barrier();
+  store_rows(hb1 - 1);
   wait_vm<0>();  // no copy into LDS outlives the workgroup
 }
 
@@ -421,9 +431,12 @@ __global__ __launch_bounds__(256) void dx_wide_kernel(GateGradP p) {
 // of 16 MF x 64.
 //  * The planes of d_logits (24 KiB a step at MF = 4) are copied into a ring
 //    of three steps, two steps ahead.
-//  * x has its rows along K: a thread loads 4 columns of 4 tokens three steps
+//  * x has its rows along K: a thread loads 4 columns of 4 tokens R steps
 //    ahead into registers, transposes them there and stores 8-byte pieces
 //    (4 tokens of a column) into the step's fragments one step ahead.  The
+//    operations of a wave complete in issue order and the compiler's waits
+//    for the loads do not know of the copies, so they cover about half of
+//    those R steps; a step's copies go out before its loads.  The
 //    16-byte slot of a fragment is XORed with the fragment's number, so that
 //    lanes which write the same slot of 8 fragments meet different banks.
 //  * Workgroups of one K split that share columns or planes run on the same
@@ -431,15 +444,14 @@ __global__ __launch_bounds__(256) void dx_wide_kernel(GateGradP p) {
 template <int MF>
 __global__ __launch_bounds__(512, 2) void d_gate_kernel(GateGradP p) {
   constexpr int AF = 3 * 2 * MF, BF = 16;
-  constexpr int N_X = 4, N_A = AF / 8;  // loads of x, and copies (at least), of a wave and step
+  constexpr int R = 6, N_X = 4, N_A = AF / 8;  // loads of x, and copies (at least), of a wave and step
   __shared__ __align__(16) uint16_t alds[3][AF * kFrag];
   __shared__ __align__(16) uint16_t blds[2][BF * kFrag];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave & 1, wn = wave >> 1;
   const int ht = (p.H + 255) / 256;
-  const int items = ht * p.mtiles * p.splits, per = (items + 7) / 8;
-  const int item = (blockIdx.x % 8) * per + blockIdx.x / 8;
-  if (blockIdx.x / 8 >= per || item >= items) return;
+  const int item = xcd_item(ht * p.mtiles * p.splits);
+  if (item < 0) return;
   const int mt = item % p.mtiles, hx = item / p.mtiles % ht, z = item / p.mtiles / ht;
   const int h0 = hx * 256;
   const int s0 = z * p.steps, n = min(p.nt32, s0 + p.steps) - s0;  // >= 1
@@ -457,7 +469,7 @@ __global__ __launch_bounds__(512, 2) void d_gate_kernel(GateGradP p) {
   // this thread's 4 tokens and 4 columns of a step
   const int quad = (wave & 3) * 2 + lane / 32, hq = (wave >> 2) * 32 + lane % 32;
   const int xcol = min(h0 + hq * 4, p.H - 4);  // (columns past H: of the last tile, not stored)
-  u32x2_t xr[3][4];
+  u32x2_t xr[R][4];
   auto load_x = [&](int s, u32x2_t(&to)[4]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -485,23 +497,27 @@ __global__ __launch_bounds__(512, 2) void d_gate_kernel(GateGradP p) {
   for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // x of step s sits in xr[s % 3]; loads past the last step read its rows again
-  load_x(0, xr[0]);
-  load_x(1, xr[1]);
+  // x of step s sits in xr[s % R]; loads past the last step read rows again
+#pragma unroll
+  for (int i = 0; i < R - 2; ++i) load_x(i, xr[i]);
   copy_a(0);
   keep_order();
-  load_x(2, xr[2]);
+  load_x(R - 2, xr[R - 2]);
   copy_a(1);
   keep_order();
+  load_x(R - 1, xr[R - 1]);
   store_x(0, xr[0]);
-  // behind step s's copies: the copies of step s + 1 and the loads of x that
-  // go with them (left out of the last step's count: nobody reads what the
-  // step before it loads, so the compiler may drop those)
-  auto step = [&](int s, u32x2_t(&next)[4], u32x2_t(&free)[4], auto behind) {
+  // BEHIND: vector memory operations behind step s's copies (issued at step
+  // s - 2): that step's loads of x, then the copies and loads of step s - 1.
+  // Steps past the unrolled loop load no x.
+  auto step = [&](int s, u32x2_t(&next)[4], u32x2_t(&free)[4], auto behind, auto loads) {
     wait_vm<decltype(behind)::value>();
     step_barrier();
-    load_x(s + 3, free);
     copy_a(s + 2);
+    keep_order();
+    if (decltype(loads)::value) load_x(s + R, free);
+    keep_order();
+    store_x(s + 1, next);
     const uint16_t* A = alds[s % 3];
     const uint16_t* B = blds[s & 1];
     bf16x8_t b[4];
@@ -515,16 +531,22 @@ __global__ __launch_bounds__(512, 2) void d_gate_kernel(GateGradP p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32_bf16(a, b[j], acc[i][j]);
       }
-    store_x(s + 1, next);
   };
   int s = 0;
-  for (; s + 3 <= n; s += 3) {
-    step(s, xr[1], xr[0], std::integral_constant<int, N_X + N_A>{});
-    step(s + 1, xr[2], xr[1], std::integral_constant<int, N_X + N_A>{});
-    step(s + 2, xr[0], xr[2], std::integral_constant<int, N_X + N_A>{});
+  for (; s + R <= n; s += R) {
+    [&]<int... I>(std::integer_sequence<int, I...>) {
+      (step(s + I, xr[(I + 1) % R], xr[I], std::integral_constant<int, 2 * N_X + N_A>{}, std::true_type{}), ...);
+    }
+    (std::make_integer_sequence<int, R>{});
   }
-  if (s < n) step(s, xr[1], xr[0], std::integral_constant<int, N_X + N_A>{});
-  if (s + 1 < n) step(s + 1, xr[2], xr[1], std::integral_constant<int, N_A>{});
+  [&]<int... I>(std::integer_sequence<int, I...>) {
+    ((s + I < n ? step(s + I, xr[(I + 1) % R], xr[I],
+                       std::integral_constant<int, I == 0 ? 2 * N_X + N_A : I == 1 ? N_X + N_A : N_A>{},
+                       std::false_type{})
+                : void()),
+     ...);
+  }
+  (std::make_integer_sequence<int, R - 1>{});
   wait_vm<0>();  // no copy into LDS outlives the workgroup
   float* out = p.splits > 1 ? p.part + (size_t)z * p.E * p.H : p.d_gate;
 #pragma unroll
@@ -606,7 +628,7 @@ GateGradPlan gate_grad_plan(int T, int H, int E) {
 
 template <int KF, int MT>
 void launch_dx_kf(const GateGradP& p, hipStream_t s) {
-  const int grid = ceil_div(p.T, 128 * MT) * p.hsplits;
+  const int grid = ceil_div(ceil_div(p.T, 128 * MT) * p.hsplits, 8) * 8;
   if (p.gate_fp32) {
     if (p.dx_in)
       dx_kernel<KF, MT, 2, true><<<grid, 512, 0, s>>>(p);
