@@ -39,9 +39,12 @@ typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
 // Buffer range at `base`: loads at or past its end give zero, stores there
 // are dropped, and either way the instruction is issued (the waits below
 // count instructions).
-__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint64_t bytes) {
-  const uint32_t n = bytes > 0xFFFFFFFFull ? 0xFFFFFFFFu : (uint32_t)bytes;
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)n, 0x00020000);
+__device__ __forceinline__ rsrc_t make_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t b = (uint64_t)base;
+  const uint64_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b);
+  const uint64_t hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+  return __builtin_amdgcn_make_buffer_rsrc(reinterpret_cast<void*>(hi << 32 | lo), 0,
+                                           __builtin_amdgcn_readfirstlane((int)bytes), 0x00020000);
 }
 // The same range as the four words of a descriptor, in scalar registers.
 __device__ __forceinline__ i32x4_t make_desc(const void* base, uint32_t bytes) {
@@ -200,6 +203,9 @@ __device__ __forceinline__ bf16x8_t frag(const uint16_t* lds, int lane) {
   return *reinterpret_cast<const bf16x8_t*>(lds + lane * 8);
 }
 
+// A division's result is in a vector register, also a uniform one's.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+
 // Item of a grid of 8 ceil(items / 8) workgroups such that each XCD
 // (workgroups are dealt to the XCDs in turn) has a contiguous run of them;
 // -1: none.
@@ -235,7 +241,7 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int item = xcd_item((p.T + ROWS - 1) / ROWS * p.hsplits);
   if (item < 0) return;
-  const int hs = item % p.hsplits, tg = item / p.hsplits;
+  const int tg = uniform(item / p.hsplits), hs = item - tg * p.hsplits;
   const int hb0 = hs * p.hper, hb1 = min(p.H / 64, hb0 + p.hper);
   const int total = (hb1 - hb0) * KF;  // >= 1
   const i32x4_t gb = make_desc(p.dxb + (size_t)hb0 * KF * SF * kFrag, (uint32_t)total * SF * kFrag * 2);
@@ -250,9 +256,9 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
   // the rows that waves 4-7 move: 8 per copy, lane l the 16-byte piece l % 8
   // (XORed) of row l / 8
   const int t0 = tg * ROWS, r0 = (wave & 3) * (ROWS / 4);
-  const uint64_t bytes = (uint64_t)min(p.T - t0, ROWS) * p.H * 2;  // of the rows below T
+  const uint32_t bytes = (uint32_t)min(p.T - t0, ROWS) * p.H * 2;  // of the rows below T
   const size_t origin = (size_t)t0 * p.H;
-  const i32x4_t in = make_desc(ADD ? p.dx_in + origin : nullptr, (uint32_t)bytes);
+  const i32x4_t in = make_desc(ADD ? p.dx_in + origin : nullptr, bytes);
   const rsrc_t out = make_rsrc(p.dx + origin, bytes);
   uint32_t row_at[RC];
 #pragma unroll
@@ -452,44 +458,51 @@ __global__ __launch_bounds__(512, 2) void d_gate_kernel(GateGradP p) {
   const int ht = (p.H + 255) / 256;
   const int item = xcd_item(ht * p.mtiles * p.splits);
   if (item < 0) return;
-  const int mt = item % p.mtiles, hx = item / p.mtiles % ht, z = item / p.mtiles / ht;
+  const int col = uniform(item / p.mtiles), mt = item - col * p.mtiles;
+  const int z = uniform(col / ht), hx = col - z * ht;
   const int h0 = hx * 256;
   const int s0 = z * p.steps, n = min(p.nt32, s0 + p.steps) - s0;  // >= 1
-  const uint32_t step_bytes = 3u * p.Ef * kFrag * 2;
-  auto copy_a = [&](int s) {  // past the end: the last step again
-    const i32x4_t r = make_desc(p.dga + (size_t)(s0 + min(s, n - 1)) * 3 * p.Ef * kFrag, step_bytes);
+  // Everything a step needs beside its operands is scalar or set up here: the
+  // descriptors move along with the steps, the offsets inside a step stay.
+  const uint32_t a_step = 3u * p.Ef * kFrag * 2;
+  const uint16_t* const a_first = p.dga + (size_t)s0 * 3 * p.Ef * kFrag;
+  uint32_t a_at[(AF + 7) / 8];
 #pragma unroll
-    for (int f0 = 0; f0 < AF; f0 += 8) {
-      const int f = f0 + wave;
-      if (f0 + 8 <= AF || f < AF)
-        copy_frag(r, (uint32_t)(((f / (2 * MF)) * p.Ef + mt * 2 * MF + f % (2 * MF)) * kFrag * 2),
-                  lds_addr(alds[s % 3] + f * kFrag), lane);
-    }
+  for (int c = 0; c < (AF + 7) / 8; ++c) {
+    const int f = c * 8 + wave;
+    a_at[c] = (uint32_t)(((f / (2 * MF)) * p.Ef + mt * 2 * MF + f % (2 * MF)) * kFrag * 2);
+  }
+  auto copy_a = [&](int s, int slot) {  // past the end: the last step again
+    const i32x4_t r = make_desc(reinterpret_cast<const char*>(a_first) + (size_t)min(s, n - 1) * a_step, a_step);
+#pragma unroll
+    for (int c = 0; c < (AF + 7) / 8; ++c)
+      if (c * 8 + 8 <= AF || c * 8 + wave < AF) copy_frag(r, a_at[c], lds_addr(alds[slot] + (c * 8 + wave) * kFrag), lane);
   };
-  // this thread's 4 tokens and 4 columns of a step
+  // this thread's 4 tokens and 4 columns of a step; rows at or past T are
+  // outside the range and read as zeros, columns past H (of the last tile)
+  // are not stored
   const int quad = (wave & 3) * 2 + lane / 32, hq = (wave >> 2) * 32 + lane % 32;
-  const int xcol = min(h0 + hq * 4, p.H - 4);  // (columns past H: of the last tile, not stored)
+  uint32_t x_at[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x_at[i] = (uint32_t)(quad * 4 + i) * p.H * 2 + min(h0 + hq * 4, p.H - 4) * 2;
   u32x2_t xr[R][4];
   auto load_x = [&](int s, u32x2_t(&to)[4]) {
+    const int t = (s0 + s) * 32, rows = max(0, min(p.T - t, 32));
+    const rsrc_t r = make_rsrc(p.x + (size_t)(rows > 0 ? t : 0) * p.H, (uint32_t)rows * p.H * 2);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int t = (s0 + s) * 32 + quad * 4 + i;
-      to[i] = *reinterpret_cast<const u32x2_t*>(p.x + (size_t)min(t, p.T - 1) * p.H + xcol);
-    }
+    for (int i = 0; i < 4; ++i) to[i] = __builtin_amdgcn_raw_buffer_load_b64(r, x_at[i], 0, 0);
   };
-  auto store_x = [&](int s, u32x2_t(&v)[4]) {
-    const int t = (s0 + s) * 32 + quad * 4;
+  uint32_t b_at[4];  // where this thread's piece of each of its columns goes, in 16-bit values
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (t + i >= p.T) v[i] = u32x2_t{0u, 0u};
-    uint16_t* B = blds[s & 1] + (hq / 4) * kFrag + (quad & 1) * 4;
+  for (int c = 0; c < 4; ++c)
+    b_at[c] = (hq / 4) * kFrag + (((quad / 2) * 16 + (hq % 4) * 4 + c) ^ (hq / 4)) * 8 + (quad & 1) * 4;
+  auto store_x = [&](int slot, const u32x2_t(&v)[4]) {
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
       const uint32_t sel = c & 1 ? 0x07060302u : 0x05040100u;
-      const u32x2_t w = {__builtin_amdgcn_perm(v[1][c / 2], v[0][c / 2], sel),
-                         __builtin_amdgcn_perm(v[3][c / 2], v[2][c / 2], sel)};
-      const int slot = ((quad / 2) * 16 + (hq % 4) * 4 + c) ^ (hq / 4);
-      *reinterpret_cast<u32x2_t*>(B + slot * 8) = w;
+      *reinterpret_cast<u32x2_t*>(blds[slot] + b_at[c]) =
+          u32x2_t{__builtin_amdgcn_perm(v[1][c / 2], v[0][c / 2], sel),
+                  __builtin_amdgcn_perm(v[3][c / 2], v[2][c / 2], sel)};
     }
   };
   f32x4_t acc[MF][4];
@@ -497,50 +510,58 @@ __global__ __launch_bounds__(512, 2) void d_gate_kernel(GateGradP p) {
   for (int i = 0; i < MF; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  // x of step s sits in xr[s % R]; loads past the last step read rows again
+  // x of step s sits in xr[s % R], its fragments in blds[s % 2], the planes
+  // in alds[s % 3]: with R a multiple of 6 all fixed in the unrolled loop
+  static_assert(R % 6 == 0, "slots by the place in the loop");
 #pragma unroll
   for (int i = 0; i < R - 2; ++i) load_x(i, xr[i]);
-  copy_a(0);
+  copy_a(0, 0);
   keep_order();
   load_x(R - 2, xr[R - 2]);
-  copy_a(1);
+  copy_a(1, 1);
   keep_order();
   load_x(R - 1, xr[R - 1]);
   store_x(0, xr[0]);
   // BEHIND: vector memory operations behind step s's copies (issued at step
   // s - 2): that step's loads of x, then the copies and loads of step s - 1.
   // Steps past the unrolled loop load no x.
-  auto step = [&](int s, u32x2_t(&next)[4], u32x2_t(&free)[4], auto behind, auto loads) {
+  auto step = [&](int s, auto place, auto behind, auto loads) {
+    constexpr int I = decltype(place)::value;
     wait_vm<decltype(behind)::value>();
     step_barrier();
-    copy_a(s + 2);
-    keep_order();
-    if (decltype(loads)::value) load_x(s + R, free);
-    keep_order();
-    store_x(s + 1, next);
-    const uint16_t* A = alds[s % 3];
-    const uint16_t* B = blds[s & 1];
+    const uint16_t* A = alds[I % 3] + wm * MF * kFrag + lane * 8;
+    const uint16_t* B = blds[I % 2] + wn * 4 * kFrag;
     bf16x8_t b[4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = frag(B + (wn * 4 + j) * kFrag, lane ^ (wn * 4 + j));
+    for (int j = 0; j < 4; ++j) b[j] = frag(B + j * kFrag, lane ^ (wn * 4 + j));
+    bf16x8_t a[3];
+#pragma unroll
+    for (int q = 0; q < 3; ++q) a[q] = frag(A + q * 2 * MF * kFrag, 0);
+    // the next steps' operands are asked for while these reads are under way
+    copy_a(s + 2, (I + 2) % 3);
+    keep_order();
+    if (decltype(loads)::value) load_x(s + R, xr[I]);
+    keep_order();
+    store_x((I + 1) % 2, xr[(I + 1) % R]);
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
       for (int q = 0; q < 3; ++q) {
-        const bf16x8_t a = frag(A + (q * 2 * MF + wm * MF + i) * kFrag, lane);
+        const bf16x8_t now = a[q];
+        if (i + 1 < MF) a[q] = frag(A + (q * 2 * MF + i + 1) * kFrag, 0);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32_bf16(a, b[j], acc[i][j]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = mfma_16x16x32_bf16(now, b[j], acc[i][j]);
       }
   };
   int s = 0;
   for (; s + R <= n; s += R) {
     [&]<int... I>(std::integer_sequence<int, I...>) {
-      (step(s + I, xr[(I + 1) % R], xr[I], std::integral_constant<int, 2 * N_X + N_A>{}, std::true_type{}), ...);
+      (step(s + I, std::integral_constant<int, I>{}, std::integral_constant<int, 2 * N_X + N_A>{}, std::true_type{}), ...);
     }
     (std::make_integer_sequence<int, R>{});
   }
   [&]<int... I>(std::integer_sequence<int, I...>) {
-    ((s + I < n ? step(s + I, xr[(I + 1) % R], xr[I],
+    ((s + I < n ? step(s + I, std::integral_constant<int, I>{},
                        std::integral_constant<int, I == 0 ? 2 * N_X + N_A : I == 1 ? N_X + N_A : N_A>{},
                        std::false_type{})
                 : void()),
