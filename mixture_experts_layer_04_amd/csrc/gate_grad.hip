@@ -126,77 +126,92 @@ struct GateGradP {
   float* part;    // [splits][E][H]
 };
 
-// d_logits -> its planes for both products: a workgroup takes 32 tokens x 64
-// experts through LDS.
-__global__ __launch_bounds__(256) void split_logits_kernel(GateGradP p) {
-  __shared__ float tile[32][65];
-  const int t0 = blockIdx.x * 32, e0 = blockIdx.y * 64;
-  {
-    const int t = t0 + threadIdx.x / 8, e = e0 + (threadIdx.x % 8) * 8;
-    uint32_t h[8], m[8], l[8];
+// 8 values from column c of a row of n, zeros past its end
+__device__ __forceinline__ void load8(const float* row, int c, int n, float (&f)[8]) {
+  if (c + 8 <= n) {
+    f32x4_t a, b;
+    __builtin_memcpy(&a, row + c, 16);
+    __builtin_memcpy(&b, row + c + 4, 16);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = t < p.T && e + i < p.E ? p.dl[(size_t)t * p.E + e + i] : 0.f;
-      tile[threadIdx.x / 8][(threadIdx.x % 8) * 8 + i] = v;
-      split3(v, h[i], m[i], l[i]);
+    for (int i = 0; i < 4; ++i) {
+      f[i] = a[i];
+      f[i + 4] = b[i];
     }
-    if (p.dxa && e / 32 < p.Kf) {  // t0 < 128 tiles_t by the grid
-      const int lane = t % 16 + 16 * ((e % 32) / 8);
-      uint16_t* at = p.dxa + (((size_t)(t / 128) * p.Kf + e / 32) * 2 * 8 + (t % 128) / 16) * kFrag + lane * 8;
-      *reinterpret_cast<u32x4_t*>(at) =
-          u32x4_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
-      *reinterpret_cast<u32x4_t*>(at + 8 * kFrag) =
-          u32x4_t{m[0] | (m[1] << 16), m[2] | (m[3] << 16), m[4] | (m[5] << 16), m[6] | (m[7] << 16)};
-    }
-  }
-  __syncthreads();
-  const int c = threadIdx.x % 64, tg = threadIdx.x / 64, e = e0 + c;
-  if (p.dga && e / 16 < p.Ef && (int)blockIdx.x < p.nt32) {
-    uint32_t h[8], m[8], l[8];
+  } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) split3(tile[tg * 8 + i][c], h[i], m[i], l[i]);
-    const int lane = e % 16 + 16 * tg;
-    uint16_t* at = p.dga + ((size_t)blockIdx.x * 3 * p.Ef + e / 16) * kFrag + lane * 8;
-    const size_t plane = (size_t)p.Ef * kFrag;
-    *reinterpret_cast<u32x4_t*>(at) =
-        u32x4_t{h[0] | (h[1] << 16), h[2] | (h[3] << 16), h[4] | (h[5] << 16), h[6] | (h[7] << 16)};
-    *reinterpret_cast<u32x4_t*>(at + plane) =
-        u32x4_t{m[0] | (m[1] << 16), m[2] | (m[3] << 16), m[4] | (m[5] << 16), m[6] | (m[7] << 16)};
-    *reinterpret_cast<u32x4_t*>(at + 2 * plane) =
-        u32x4_t{l[0] | (l[1] << 16), l[2] | (l[3] << 16), l[4] | (l[5] << 16), l[6] | (l[7] << 16)};
+    for (int i = 0; i < 8; ++i) f[i] = c + i < n ? row[c + i] : 0.f;
   }
 }
+// 8 values' planes, one 16-byte piece each, `plane` values apart
+template <int N>
+__device__ __forceinline__ void store_planes(const float (&f)[8], uint16_t* at, size_t plane) {
+  uint32_t v[3][8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) split3(f[i], v[0][i], v[1][i], v[2][i]);
+#pragma unroll
+  for (int q = 0; q < N; ++q)
+    *reinterpret_cast<u32x4_t*>(at + q * plane) = u32x4_t{v[q][0] | (v[q][1] << 16), v[q][2] | (v[q][3] << 16),
+                                                          v[q][4] | (v[q][5] << 16), v[q][6] | (v[q][7] << 16)};
+}
 
-// The gate's planes with rows h: a workgroup takes 32 experts x 64 columns.
-__global__ __launch_bounds__(256) void split_gate_kernel(GateGradP p) {
+// The planes of both products in one launch, a tile of 32 x 64 values
+// through LDS per workgroup: the first `logit_tiles` workgroups take d_logits
+// (32 tokens x 64 experts: rows t for dx as they are, rows e for d_gate
+// across), the others the gate (32 experts x 64 columns, across).
+__global__ __launch_bounds__(256) void split_kernel(GateGradP p, int logit_tiles, int e_tiles) {
   __shared__ float tile[32][65];
-  const int e0 = blockIdx.x * 32, h0 = blockIdx.y * 64;
-  {
-    const int e = e0 + threadIdx.x / 8, h = h0 + (threadIdx.x % 8) * 8;
+  const int r = threadIdx.x / 8, c8 = (threadIdx.x % 8) * 8;    // loads: row, 8 columns
+  const int c = threadIdx.x % 64, g8 = (threadIdx.x / 64) * 8;  // across: column, 8 rows
+  float f[8];
+  if ((int)blockIdx.x < logit_tiles) {
+    const int bt = blockIdx.x / e_tiles, t = bt * 32 + r, e0 = (blockIdx.x % e_tiles) * 64;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      float v = 0.f;
-      if (e < p.E) {
-        const size_t at = (size_t)e * p.H + h + i;
-        v = p.gate_fp32 ? static_cast<const float*>(p.gate)[at]
-                        : bf16_to_f32(static_cast<const uint16_t*>(p.gate)[at]);
-      }
-      tile[threadIdx.x / 8][(threadIdx.x % 8) * 8 + i] = v;
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    if (t < p.T) load8(p.dl + (size_t)t * p.E, e0 + c8, p.E, f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tile[r][c8 + i] = f[i];
+    const int e = e0 + c8;
+    if (p.dxa && e / 32 < p.Kf)  // t < 128 tiles_t by the grid
+      store_planes<2>(f,
+                      p.dxa + (((size_t)(t / 128) * p.Kf + e / 32) * 2 * 8 + (t % 128) / 16) * kFrag +
+                          (t % 16 + 16 * ((e % 32) / 8)) * 8,
+                      8 * kFrag);
+    __syncthreads();
+    if (p.dga && (e0 + c) / 16 < p.Ef && bt < p.nt32) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) f[i] = tile[g8 + i][c];
+      store_planes<3>(f, p.dga + ((size_t)bt * 3 * p.Ef + (e0 + c) / 16) * kFrag + (c % 16 + 16 * (g8 / 8)) * 8,
+                      (size_t)p.Ef * kFrag);
     }
-  }
-  __syncthreads();
-  const int c = threadIdx.x % 64, eg = threadIdx.x / 64, h = h0 + c;
-  uint32_t a[8], m[8], l[8];
+  } else {
+    const int b = blockIdx.x - logit_tiles, be = b % p.Kf, e = be * 32 + r, h = b / p.Kf * 64 + c8;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) split3(tile[eg * 8 + i][c], a[i], m[i], l[i]);
-  const int planes = p.gate_fp32 ? 2 : 1, lane = h % 16 + 16 * eg;
-  uint16_t* at =
-      p.dxb + (((size_t)(h / 64) * p.Kf + blockIdx.x) * planes * 4 + (h % 64) / 16) * kFrag + lane * 8;
-  *reinterpret_cast<u32x4_t*>(at) =
-      u32x4_t{a[0] | (a[1] << 16), a[2] | (a[3] << 16), a[4] | (a[5] << 16), a[6] | (a[7] << 16)};
-  if (planes == 2)
-    *reinterpret_cast<u32x4_t*>(at + 4 * kFrag) =
-        u32x4_t{m[0] | (m[1] << 16), m[2] | (m[3] << 16), m[4] | (m[5] << 16), m[6] | (m[7] << 16)};
+    for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    if (e < p.E) {
+      if (p.gate_fp32) {
+        load8(static_cast<const float*>(p.gate) + (size_t)e * p.H, h, p.H, f);
+      } else {
+        const u32x4_t u = *reinterpret_cast<const u32x4_t*>(static_cast<const uint16_t*>(p.gate) + (size_t)e * p.H + h);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          f[2 * i] = bf16_lo(u[i]);
+          f[2 * i + 1] = bf16_hi(u[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tile[r][c8 + i] = f[i];
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = tile[g8 + i][c];
+    const int planes = p.gate_fp32 ? 2 : 1;
+    uint16_t* at =
+        p.dxb + ((size_t)(b / p.Kf) * p.Kf + be) * planes * 4 * kFrag + (c / 16) * kFrag + (c % 16 + 16 * (g8 / 8)) * 8;
+    if (planes == 2)
+      store_planes<2>(f, at, 4 * kFrag);
+    else
+      store_planes<1>(f, at, 0);
+  }
 }
 
 __device__ __forceinline__ bf16x8_t frag(const uint16_t* lds, int lane) {
@@ -217,7 +232,8 @@ __device__ __forceinline__ int xcd_item(int items) {
 // dx up to 512 experts: a wave keeps both planes of its 16 MT tokens in
 // registers (all KF steps of them) and the workgroup, 8 waves of different
 // tokens, streams the gate's planes through an LDS ring: per 64 columns, KF
-// stages of 4 GP fragments, in memory order, asked for D - 1 steps ahead.
+// steps of 4 GP fragments, SK of them a stage, in memory order, asked for
+// D - 1 stages ahead.
 // The gate is the MFMA's row operand, so a lane holds 4 consecutive columns
 // of a token.
 //
@@ -234,7 +250,10 @@ __device__ __forceinline__ int xcd_item(int items) {
 // groups that run beside each other.
 template <int KF, int MT, int GP, bool ADD>
 __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
-  constexpr int D = 8, SF = 4 * GP, ROWS = 8 * MT * 16;
+  // K steps per ring stage and barrier: with one of them (24 MFMAs a wave at
+  // MT 2) a wave spends as long on the barrier and the first LDS reads
+  constexpr int SK = KF % 2 == 0 ? 2 : KF % 3 == 0 ? 3 : 1;
+  constexpr int D = SK == 1 ? 8 : SK == 2 ? 4 : 3, SF = 4 * GP * SK, ROWS = 8 * MT * 16;
   constexpr int RC = ROWS / 4 / 8;  // 1 KiB copies (8 rows) of a row-moving wave and block
   __shared__ __align__(16) uint16_t ring[D][SF * kFrag];
   __shared__ __align__(16) uint16_t rowbuf[2][ROWS * 64];
@@ -243,14 +262,14 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
   if (item < 0) return;
   const int tg = uniform(item / p.hsplits), hs = item - tg * p.hsplits;
   const int hb0 = hs * p.hper, hb1 = min(p.H / 64, hb0 + p.hper);
-  const int total = (hb1 - hb0) * KF;  // >= 1
-  const i32x4_t gb = make_desc(p.dxb + (size_t)hb0 * KF * SF * kFrag, (uint32_t)total * SF * kFrag * 2);
+  const int total = (hb1 - hb0) * (KF / SK);  // stages, >= 1
+  const i32x4_t gb = make_desc(p.dxb + (size_t)hb0 * KF * 4 * GP * kFrag, (uint32_t)total * SF * kFrag * 2);
   auto copy = [&](int s) {  // past the end: the last stage again, into a slot nobody reads
     if (wave < 4) {
 #pragma unroll
-      for (int i = 0; i < GP; ++i)
-        copy_frag(gb, (uint32_t)((min(s, total - 1) * SF + wave * GP + i) * kFrag * 2),
-                  lds_addr(ring[s % D] + (wave * GP + i) * kFrag), lane);
+      for (int i = 0; i < GP * SK; ++i)
+        copy_frag(gb, (uint32_t)((min(s, total - 1) * SF + wave * GP * SK + i) * kFrag * 2),
+                  lds_addr(ring[s % D] + (wave * GP * SK + i) * kFrag), lane);
     }
   };
   // the rows that waves 4-7 move: 8 per copy, lane l the 16-byte piece l % 8
@@ -294,7 +313,7 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
       tm[m][k] = *reinterpret_cast<const bf16x8_t*>(at + (size_t)(k * 16 + 8) * kFrag);
     }
   }
-  int done = 0;  // steps
+  int done = 0;  // stages
   for (int hb = hb0; hb < hb1; ++hb) {
     f32x4_t acc[4][MT];
 #pragma unroll
@@ -308,9 +327,9 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
       // dx_in has when only the stores and dx_in copies of this block's
       // first step are (with one step a block, those come after the wait).
       if (wave < 4)
-        wait_vm<(D - 2) * GP>();
-      else if (ADD && k == KF - 1)
-        hb == hb0 ? wait_vm<KF == 1 ? 0 : RC>() : wait_vm<KF == 1 ? 0 : 2 * RC>();
+        wait_vm<(D - 2) * GP * SK>();
+      else if (ADD && k == KF / SK - 1)
+        hb == hb0 ? wait_vm<KF == SK ? 0 : RC>() : wait_vm<KF == SK ? 0 : 2 * RC>();
       step_barrier();  // all of that is there for every wave; the step before is read
       copy(done + D - 1);
       if (k == 0) {
@@ -319,25 +338,29 @@ __global__ __launch_bounds__(512, 2) void dx_kernel(GateGradP p) {
         asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
         copy_rows(hb + 1);
       }
-      const uint16_t* B = ring[done % D];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const bf16x8_t gh = frag(B + i * kFrag, lane);
+      for (int kk = 0; kk < SK; ++kk) {
+        const uint16_t* B = ring[done % D] + kk * 4 * GP * kFrag;
+        const int q = k * SK + kk;
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          acc[i][m] = mfma_16x16x32_bf16(gh, th[m][k], acc[i][m]);
-          acc[i][m] = mfma_16x16x32_bf16(gh, tm[m][k], acc[i][m]);
-        }
-        if (GP == 2) {
-          const bf16x8_t gm = frag(B + (4 + i) * kFrag, lane);
+        for (int i = 0; i < 4; ++i) {
+          const bf16x8_t gh = frag(B + i * kFrag, lane);
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[i][m] = mfma_16x16x32_bf16(gm, th[m][k], acc[i][m]);
+          for (int m = 0; m < MT; ++m) {
+            acc[i][m] = mfma_16x16x32_bf16(gh, th[m][q], acc[i][m]);
+            acc[i][m] = mfma_16x16x32_bf16(gh, tm[m][q], acc[i][m]);
+          }
+          if (GP == 2) {
+            const bf16x8_t gm = frag(B + (4 + i) * kFrag, lane);
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[i][m] = mfma_16x16x32_bf16(gm, th[m][q], acc[i][m]);
+          }
         }
       }
       ++done;
     };
     [&]<int... K>(std::integer_sequence<int, K...>) { (step(std::integral_constant<int, K>{}), ...); }
-    (std::make_integer_sequence<int, KF>{});
+    (std::make_integer_sequence<int, KF / SK>{});
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -722,11 +745,11 @@ extern "C" moe_status moe_gate_grad(const void* x, const void* gate, int gate_is
   p.dga = d_gate ? reinterpret_cast<uint16_t*>(b + L.dga) : nullptr;
   p.part = reinterpret_cast<float*>(b + L.part);
   const int cols = p.Kf * 32 > p.Ef * 16 ? p.Kf * 32 : p.Ef * 16;
-  split_logits_kernel<<<dim3((unsigned)p.tiles_t * 4, (unsigned)ceil_div(cols, 64)), 256, 0, stream>>>(p);
+  const int e_tiles = ceil_div(cols, 64), logit_tiles = p.tiles_t * 4 * e_tiles;
+  const int gate_tiles = dx ? p.Kf * (H / 64) : 0;
+  split_kernel<<<logit_tiles + gate_tiles, 256, 0, stream>>>(p, logit_tiles, e_tiles);
   MOE_CHECK_LAUNCH();
   if (dx) {
-    split_gate_kernel<<<dim3((unsigned)p.Kf, (unsigned)(H / 64)), 256, 0, stream>>>(p);
-    MOE_CHECK_LAUNCH();
     if (p.mt == 0) {
       const dim3 grid((unsigned)(H / 128), (unsigned)(p.tiles_t < 65535 ? p.tiles_t : 65535));
       if (gate_is_fp32)
