@@ -620,6 +620,39 @@ __global__ __launch_bounds__(256) void zero_kernel(f32x4_t* out, size_t len4) {
     out[i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
 }
 
+// d_gate's tile height (mf) and K splits: the least of an estimate of its time
+// in us, per round of 256 workgroups a start and the steps, and for more than
+// one split the launch that adds them up and the bytes they write and read.
+// Fitted to a sweep of both over eleven shapes (1 to 8192 tokens, 64 to 288
+// experts), where its choice was within 3 us of the best of each; splitting
+// to fill the chip with the tallest tiles alone took 23 us instead of 14 at
+// 512 tokens, 4096 columns and 288 experts.
+void d_gate_split(GateGradP& p) {
+  static const double kStep[kMaxMf] = {0.45, 0.58, 0.82, 1.03};  // us per step by mf
+  static const int kSplits[] = {1, 2, 3, 4, 6, 8, 12, 16, 24, 32, 48, 64};
+  const int ht = ceil_div(p.H, 256), nt = p.nt32 > 0 ? p.nt32 : 1;
+  const double write = (double)p.E * p.H * 4 / 5.5e6;  // us for one array of partial sums
+  double best = 0;
+  for (int mf = 1; mf <= kMaxMf; ++mf) {
+    const int mtiles = ceil_div(p.E, 32 * mf);
+    for (int splits : kSplits) {
+      if (splits > nt) break;
+      const int steps = ceil_div(nt, splits), n = ceil_div(nt, steps);
+      const int64_t rounds = ceil_div64((int64_t)ht * mtiles * n, 256);
+      const double us = rounds * (3.0 + steps * kStep[mf - 1]) +
+                        (n > 1 ? 3.0 + 0.15 * n + (2 * n + 1) * write : write);
+      if (best == 0 || us < best) {
+        best = us;
+        p.mf = mf;
+        p.mtiles = mtiles;
+        p.steps = steps;
+        p.splits = n;
+      }
+    }
+  }
+  p.Ef = p.mtiles * 2 * p.mf;
+}
+
 // Shape-derived numbers and the workspace (offsets; 0-size parts included).
 struct GateGradPlan {
   GateGradP p;
@@ -643,18 +676,7 @@ GateGradPlan gate_grad_plan(int T, int H, int E) {
   if (p.hsplits > blocks) p.hsplits = blocks;
   p.hper = ceil_div(blocks, p.hsplits);
   p.hsplits = ceil_div(blocks, p.hper);
-  // d_gate
-  p.mtiles = ceil_div(E, 32 * kMaxMf);
-  p.mf = ceil_div(ceil_div(E, p.mtiles), 32);
-  p.Ef = p.mtiles * 2 * p.mf;
-  // about one workgroup per CU, at least 4 steps each
-  const int tiles = ceil_div(H, 256) * p.mtiles;
-  int splits = 256 / tiles;
-  const int most = ceil_div(p.nt32, 4);
-  if (splits > most) splits = most;
-  if (splits < 1) splits = 1;
-  p.steps = ceil_div(p.nt32 > 0 ? p.nt32 : 1, splits);
-  p.splits = ceil_div(p.nt32 > 0 ? p.nt32 : 1, p.steps);
+  d_gate_split(p);
   size_t off = kCtrlBytes;  // the control block stays as it is
   auto take = [&](size_t bytes) {
     const size_t at = off;
