@@ -17,8 +17,7 @@
 // Both are bound by memory: one pass, a row lives in registers between its
 // loads and its stores.  All row vectors are 16-byte accesses at the
 // alignment of an element (the hardware takes them at any address), so odd
-// widths keep the wide accesses; only the last vector of a row that 8 does
-// not divide goes element by element.
+// widths keep the wide accesses.
 
 #include <cmath>
 #include <type_traits>
@@ -31,67 +30,128 @@ namespace moe {
 
 namespace {
 
-constexpr int kMaxNormH = 32768;  // 16 waves x 4 vectors x 8 values
+constexpr int kMaxNormH = 32768;  // 16 waves x 64 lanes x 4 vectors x 8 values
 constexpr int kVec = 8;           // values per vector
 
-// 8 values from element i of a row of n (zeros past its end)
-__device__ __forceinline__ void load8(const uint16_t* row, int i, int n, float (&f)[8]) {
-  if (i + kVec <= n) {
-    u32x4_t v;
-    __builtin_memcpy(&v, row + i, 16);
+// The 8 values of a row of n that a thread's vector i (its first element)
+// stands for.  A vector that runs past the row's end is moved back to end
+// with it: its first `skip` values are its neighbour's, which are left out of
+// sums and scales and stored twice with the same value.  Rows of fewer than
+// 8 values go element by element.
+struct Span {
+  int base, skip;  // skip 8: no vector
+};
+__device__ __forceinline__ Span span_of(int i, int n) {
+  if (i >= n) return Span{0, 8};
+  if (i + kVec <= n || n < kVec) return Span{i, 0};
+  return Span{n - kVec, i + kVec - n};
+}
+
+// A vector as it comes from memory (bf16: two values a word).
+template <class T>
+struct Raw;
+template <>
+struct Raw<uint16_t> {
+  u32x4_t v;
+  __device__ __forceinline__ void load(const uint16_t* row, Span s, int n) {
+    v = u32x4_t{0u, 0u, 0u, 0u};
+    if (s.skip == 8) return;
+    if (n >= kVec) {
+      __builtin_memcpy(&v, row + s.base, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (j < n) v[j / 2] |= (uint32_t)row[j] << (16 * (j & 1));
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f[2 * j] = bf16_lo(v[j]);
       f[2 * j + 1] = bf16_hi(v[j]);
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = i + j < n ? bf16_to_f32(row[i + j]) : 0.f;
   }
-}
-__device__ __forceinline__ void load8(const float* row, int i, int n, float (&f)[8]) {
-  if (i + kVec <= n) {
-    f32x4_t a, b;
-    __builtin_memcpy(&a, row + i, 16);
-    __builtin_memcpy(&b, row + i + 4, 16);
+};
+template <>
+struct Raw<float> {
+  f32x4_t a, b;
+  __device__ __forceinline__ void load(const float* row, Span s, int n) {
+    a = b = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    if (s.skip == 8) return;
+    if (n >= kVec) {
+      __builtin_memcpy(&a, row + s.base, 16);
+      __builtin_memcpy(&b, row + s.base + 4, 16);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if (j < n) a[j] = row[j];
+        if (j + 4 < n) b[j] = row[j + 4];
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&f)[8]) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       f[j] = a[j];
       f[j + 4] = b[j];
     }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) f[j] = i + j < n ? row[i + j] : 0.f;
   }
-}
-__device__ __forceinline__ void store8(uint16_t* row, int i, int n, const float (&f)[8]) {
+};
+typedef u32x4_t u32x4_any_t __attribute__((aligned(2)));
+typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
+// once: nobody reads the values soon (a hint to the caches)
+__device__ __forceinline__ void store8(uint16_t* row, Span s, int n, const float (&f)[8], bool once = false) {
+  if (s.skip == 8) return;
   u32x4_t v;
 #pragma unroll
   for (int j = 0; j < 4; ++j) v[j] = cvt_bf16x2(f[2 * j], f[2 * j + 1]);
-  if (i + kVec <= n) {
-    __builtin_memcpy(row + i, &v, 16);
+  if (n >= kVec) {
+    u32x4_any_t* at = reinterpret_cast<u32x4_any_t*>(row + s.base);
+    if (once)
+      __builtin_nontemporal_store(v, at);
+    else
+      *at = v;
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (i + j < n) row[i + j] = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
+      if (j < n) row[j] = (uint16_t)(v[j / 2] >> (16 * (j & 1)));
   }
 }
-__device__ __forceinline__ void store8(float* row, int i, int n, const float (&f)[8]) {
-  if (i + kVec <= n) {
+__device__ __forceinline__ void store8(float* row, Span s, int n, const float (&f)[8], bool once = false) {
+  if (s.skip == 8) return;
+  if (n >= kVec) {
     const f32x4_t a = {f[0], f[1], f[2], f[3]}, b = {f[4], f[5], f[6], f[7]};
-    __builtin_memcpy(row + i, &a, 16);
-    __builtin_memcpy(row + i + 4, &b, 16);
+    f32x4_any_t* at = reinterpret_cast<f32x4_any_t*>(row + s.base);
+    if (once) {
+      __builtin_nontemporal_store(a, at);
+      __builtin_nontemporal_store(b, at + 1);
+    } else {
+      at[0] = a;
+      at[1] = b;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j)
-      if (i + j < n) row[i + j] = f[j];
+      if (j < n) row[j] = f[j];
   }
 }
-__device__ __forceinline__ void load_weight8(const void* w, int w_fp32, int i, int n, float (&f)[8]) {
-  if (w_fp32)
-    load8(static_cast<const float*>(w), i, n, f);
-  else
-    load8(static_cast<const uint16_t*>(w), i, n, f);
+__device__ __forceinline__ void load_weight8(const void* w, int w_fp32, Span s, int n, float (&f)[8]) {
+  if (w_fp32) {
+    Raw<float> r;
+    r.load(static_cast<const float*>(w), s, n);
+    r.get(f);
+  } else {
+    Raw<uint16_t> r;
+    r.load(static_cast<const uint16_t*>(w), s, n);
+    r.get(f);
+  }
+}
+// a thread's sum over a moved vector starts behind its neighbour's values
+__device__ __forceinline__ float sum8(const float (&f)[8], int skip) {
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) s += j >= skip ? f[j] : 0.f;
+  return s;
 }
 
 struct NormP {
@@ -106,6 +166,7 @@ struct NormP {
   float eps, inv_h;
   int w_fp32;
   int waves;  // waves per row
+  bool once;  // outputs past the caches: store them with the hint
 };
 
 // e4m3 codes and scales of 8 values of a row; a scale group is 16 (FP8: 128
@@ -142,45 +203,47 @@ __device__ __forceinline__ void quant8(const NormP& p, size_t row, int i, const 
 }
 
 // RT: residual type, 0 none, 1 bf16, 2 fp32.  NV vectors per thread, `waves`
-// waves per row; a workgroup of 256 threads takes 4 / waves rows where a row
-// has fewer than 4 waves, else one row.
+// waves per row, as many rows per workgroup as its size holds.
 template <int NV, int QF, int RT>
-__global__ void norm_kernel(NormP p) {
+__global__ __launch_bounds__(1024) void norm_kernel(NormP p) {
+  typedef typename std::conditional<RT == 2, float, uint16_t>::type ResT;
   const int lanes = p.waves * kWave;  // threads per row
   const int sub = threadIdx.x / lanes, tid = threadIdx.x - sub * lanes;
   const int rows = blockDim.x / lanes;
   const size_t row = (size_t)blockIdx.x * rows + sub;
   const bool live = row < (size_t)p.T;
-  float h[NV][8];
+  const bool moved = p.H % kVec != 0;
+  Span sp[NV];
+#pragma unroll
+  for (int v = 0; v < NV; ++v) sp[v] = span_of((v * lanes + tid) * kVec, p.H);
+  float h[NV][8], w[NV][8];
   float ss = 0.f;
   if (live) {
-    const uint16_t* x = p.x + row * p.H;
+    Raw<uint16_t> x[NV];
+    Raw<ResT> res[NV];
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = (v * lanes + tid) * kVec;
-      load8(x, i, p.H, h[v]);
-    }
+    for (int v = 0; v < NV; ++v) x[v].load(p.x + row * p.H, sp[v], p.H);
     if (RT != 0) {
 #pragma unroll
-      for (int v = 0; v < NV; ++v) {
-        const int i = (v * lanes + tid) * kVec;
+      for (int v = 0; v < NV; ++v) res[v].load(static_cast<const ResT*>(p.res) + row * p.H, sp[v], p.H);
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v) load_weight8(p.w, p.w_fp32, sp[v], p.H, w[v]);
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      x[v].get(h[v]);
+      if (RT != 0) {
         float r[8];
-        if (RT == 1)
-          load8(static_cast<const uint16_t*>(p.res) + row * p.H, i, p.H, r);
-        else
-          load8(static_cast<const float*>(p.res) + row * p.H, i, p.H, r);
+        res[v].get(r);
 #pragma unroll
         for (int j = 0; j < 8; ++j) h[v][j] += r[j];
       }
+      float sq[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sq[j] = h[v][j] * h[v][j];
+      ss += moved ? sum8(sq, sp[v].skip) : sum8(sq, 0);
     }
-#pragma unroll
-    for (int v = 0; v < NV; ++v)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) ss += h[v][j] * h[v][j];
   }
-  float w[NV][8];
-#pragma unroll
-  for (int v = 0; v < NV; ++v) load_weight8(p.w, p.w_fp32, (v * lanes + tid) * kVec, p.H, w[v]);
   ss = wave_sum_u(ss);
   if (p.waves > 1) {
     __shared__ float part[16];
@@ -193,18 +256,12 @@ __global__ void norm_kernel(NormP p) {
   const float r = rsqrtf(ss * p.inv_h + p.eps);
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    const int i = (v * lanes + tid) * kVec;
-    if (RT != 0 && p.h && i < p.H) {
-      if (RT == 1)
-        store8(static_cast<uint16_t*>(p.h) + row * p.H, i, p.H, h[v]);
-      else
-        store8(static_cast<float*>(p.h) + row * p.H, i, p.H, h[v]);
-    }
+    if (RT != 0 && p.h) store8(static_cast<ResT*>(p.h) + row * p.H, sp[v], p.H, h[v], p.once);
     float y[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) y[j] = h[v][j] * r * w[v][j];
-    if (p.y && i < p.H) store8(p.y + row * p.H, i, p.H, y);
-    if (QF != 0) quant8<QF>(p, row, i, y);
+    if (p.y) store8(p.y + row * p.H, sp[v], p.H, y, p.once);
+    if (QF != 0) quant8<QF>(p, row, (v * lanes + tid) * kVec, y);
   }
 }
 
@@ -235,129 +292,198 @@ struct NormGradP {
   int T, H;
   float eps, inv_h;
   int w_fp32;
+  int waves;  // waves per row
 };
 
-// One workgroup per row at a time, rows blockIdx.x, + gridDim.x, ...; a
-// thread keeps the same columns for every row, so the weight and the weight
-// gradient's sums stay in its registers.
+// A workgroup holds blockDim / (64 waves) rows at a time, and takes the next
+// ones gridDim further on; a thread keeps the same columns for every row, so
+// the weight and the weight gradient's sums stay in its registers (the rows'
+// sums are added in LDS at the end, in order).  The next rows are on their
+// way while a row is reduced and stored.
 template <int NV, bool HF32>
-__global__ void norm_grad_kernel(NormGradP p) {
+__global__ __launch_bounds__(1024) void norm_grad_kernel(NormGradP p) {
   typedef typename std::conditional<HF32, float, uint16_t>::type HT;
-  const int lanes = blockDim.x, nw = lanes / kWave;
+  const int lanes = p.waves * kWave;
+  const int sub = threadIdx.x / lanes, tid = threadIdx.x - sub * lanes;
+  const int rows = blockDim.x / lanes;
+  const bool moved = p.H % kVec != 0;
   __shared__ float part[2][2][16];
-  float w[NV][8], dw[NV][8];
+  // at NV 4 the registers hold no weight beside the rest: read per row (L1)
+  constexpr bool AHEAD = NV == 1, KEEP_W = NV <= 2;
+  Span sp[NV];
+  float w[KEEP_W ? NV : 1][8], dw[NV][8];
 #pragma unroll
   for (int v = 0; v < NV; ++v) {
-    load_weight8(p.w, p.w_fp32, (v * lanes + threadIdx.x) * kVec, p.H, w[v]);
+    sp[v] = span_of((v * lanes + tid) * kVec, p.H);
+    if (KEEP_W) load_weight8(p.w, p.w_fp32, sp[v], p.H, w[v]);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[v][j] = 0.f;
   }
-  int flip = 0;
-  for (size_t row = blockIdx.x; row < (size_t)p.T; row += gridDim.x, flip ^= 1) {
-    const size_t at = row * p.H;
-    float h[NV][8], dy[NV][8];
-    float ss = 0.f, gh = 0.f;
+  Raw<HT> hr[NV], dhr[NV], hn[NV], dhn[NV];
+  Raw<uint16_t> dyr[NV], dyn[NV];
+  auto load = [&](int64_t row, Raw<HT>(&h)[NV], Raw<uint16_t>(&dy)[NV], Raw<HT>(&dh)[NV]) {
+    if (row >= p.T) return;
+    const size_t at = (size_t)row * p.H;
 #pragma unroll
     for (int v = 0; v < NV; ++v) {
-      const int i = (v * lanes + threadIdx.x) * kVec;
-      load8(static_cast<const HT*>(p.h) + at, i, p.H, h[v]);
-      load8(p.dy + at, i, p.H, dy[v]);
+      h[v].load(static_cast<const HT*>(p.h) + at, sp[v], p.H);
+      dy[v].load(p.dy + at, sp[v], p.H);
+      if (p.dh) dh[v].load(static_cast<const HT*>(p.dh) + at, sp[v], p.H);
     }
+  };
+  int flip = 0;
+  int64_t row = (int64_t)blockIdx.x * rows + sub;
+  const int64_t stride = (int64_t)gridDim.x * rows;
+  if (AHEAD) load(row, hr, dyr, dhr);
+  // every wave of the workgroup takes the same number of turns
+  for (int64_t first = (int64_t)blockIdx.x * rows; first < p.T; first += stride, row += stride, flip ^= 1) {
+    if (AHEAD)
+      load(row + stride, hn, dyn, dhn);
+    else
+      load(row, hr, dyr, dhr);
+    const bool live = row < p.T;
+    float h[NV][8], g[NV][8];
+    float ss = 0.f, gh = 0.f;
+    if (live) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v)
+      for (int v = 0; v < NV; ++v) {
+        hr[v].get(h[v]);
+        dyr[v].get(g[v]);
+        float a[8], b[8];
+        if (!KEEP_W) load_weight8(p.w, p.w_fp32, sp[v], p.H, w[0]);
+        const float(&wv)[8] = w[KEEP_W ? v : 0];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        ss += h[v][j] * h[v][j];
-        gh += dy[v][j] * w[v][j] * h[v][j];
+        for (int j = 0; j < 8; ++j) {
+          a[j] = h[v][j] * h[v][j];
+          b[j] = g[v][j] * wv[j] * h[v][j];
+        }
+        ss += moved ? sum8(a, sp[v].skip) : sum8(a, 0);
+        gh += moved ? sum8(b, sp[v].skip) : sum8(b, 0);
       }
+    }
     ss = wave_sum_u(ss);
     gh = wave_sum_u(gh);
-    if (nw > 1) {
+    if (p.waves > 1) {
       if ((threadIdx.x & 63) == 0) {
         part[flip][0][threadIdx.x >> 6] = ss;
         part[flip][1][threadIdx.x >> 6] = gh;
       }
-      // one barrier a row: a wave writes the other half next time, and this
-      // half again only after the next row's barrier
+      // one barrier a turn: a wave writes the other half next time, and this
+      // half again only after the next turn's barrier
       __syncthreads();
       ss = gh = 0.f;
-      for (int i = 0; i < nw; ++i) {
-        ss += part[flip][0][i];
-        gh += part[flip][1][i];
+      for (int i = 0; i < p.waves; ++i) {
+        ss += part[flip][0][sub * p.waves + i];
+        gh += part[flip][1][sub * p.waves + i];
       }
     }
-    const float r = rsqrtf(ss * p.inv_h + p.eps);
-    const float c = r * r * r * (gh * p.inv_h);
+    if (live) {
+      const float r = rsqrtf(ss * p.inv_h + p.eps);
+      const float c = r * r * r * (gh * p.inv_h);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = (v * lanes + threadIdx.x) * kVec;
-      float d[8];
-      if (p.dh) load8(static_cast<const HT*>(p.dh) + at, i, p.H, d);
+      for (int v = 0; v < NV; ++v) {
+        float d[8], dh[8];
+        if (p.dh) dhr[v].get(dh);
+        if (!KEEP_W) load_weight8(p.w, p.w_fp32, sp[v], p.H, w[0]);
+        const float(&wv)[8] = w[KEEP_W ? v : 0];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float n = r * (dy[v][j] * w[v][j]) - h[v][j] * c;
-        d[j] = p.dh ? n + d[j] : n;
-        dw[v][j] += dy[v][j] * (h[v][j] * r);
+        for (int j = 0; j < 8; ++j) {
+          const float n = r * (g[v][j] * wv[j]) - h[v][j] * c;
+          d[j] = p.dh ? n + dh[j] : n;
+          dw[v][j] += g[v][j] * (h[v][j] * r);
+        }
+        store8(static_cast<HT*>(p.dx) + (size_t)row * p.H, sp[v], p.H, d);
       }
-      if (i < p.H) store8(static_cast<HT*>(p.dx) + at, i, p.H, d);
     }
-  }
-  if (p.part) {
+    if (AHEAD) {
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int i = (v * lanes + threadIdx.x) * kVec;
-      if (i < p.H) store8(p.part + (size_t)blockIdx.x * p.H, i, p.H, dw[v]);
+      for (int v = 0; v < NV; ++v) {
+        hr[v] = hn[v];
+        dyr[v] = dyn[v];
+        dhr[v] = dhn[v];
+      }
     }
   }
+  if (!p.part) return;
+  if (rows > 1) {
+    extern __shared__ float sums[];  // [rows][NV][lanes][8]
+    const int width = NV * lanes * kVec;
+    __syncthreads();
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sums[sub * width + (j * NV + v) * lanes + tid] = dw[v][j];
+    __syncthreads();
+    if (sub > 0) return;
+    for (int i = 1; i < rows; ++i)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dw[v][j] += sums[i * width + (j * NV + v) * lanes + tid];
+  }
+#pragma unroll
+  for (int v = 0; v < NV; ++v) store8(p.part + (size_t)blockIdx.x * p.H, sp[v], p.H, dw[v]);
 }
 
-// out[c] = sum of n rows of part[., c], in a fixed order: 4 slices of the
-// rows per workgroup of 64 columns, then the slices.  n = 0: zeros.
+// out[c] = sum of n rows of part[., c], in a fixed order: 32 slices of the
+// rows per workgroup of 32 columns, then the slices.  n = 0: zeros.
 __global__ __launch_bounds__(256) void column_sum_kernel(const float* part, int n, int H, float* out) {
-  __shared__ float s[16][64];
-  const int c = blockIdx.x * 64 + (threadIdx.x & 15) * 4, slice = threadIdx.x >> 4;
+  __shared__ float s[32][33];
+  const int q = threadIdx.x & 7, c = blockIdx.x * 32 + q * 4, slice = threadIdx.x >> 3;
   f32x4_t acc = {0.f, 0.f, 0.f, 0.f};
-  for (int r = slice; r < n; r += 16) {
-    const float* row = part + (size_t)r * H;
-    if (c + 4 <= H) {
+  if (c + 4 <= H) {
+#pragma unroll 4
+    for (int r = slice; r < n; r += 32) {
       f32x4_t v;
-      __builtin_memcpy(&v, row + c, 16);
+      __builtin_memcpy(&v, part + (size_t)r * H + c, 16);
       acc += v;
-    } else {
-      for (int j = 0; j < 4; ++j)
-        if (c + j < H) acc[j] += row[c + j];
     }
+  } else {
+    for (int r = slice; r < n; r += 32)
+      for (int j = 0; j < 4; ++j)
+        if (c + j < H) acc[j] += part[(size_t)r * H + c + j];
   }
 #pragma unroll
-  for (int j = 0; j < 4; ++j) s[slice][(threadIdx.x & 15) * 4 + j] = acc[j];
+  for (int j = 0; j < 4; ++j) s[slice][q * 4 + j] = acc[j];
   __syncthreads();
-  const int col = blockIdx.x * 64 + threadIdx.x;
-  if (threadIdx.x < 64 && col < H) {
+  const int col = blockIdx.x * 32 + threadIdx.x;
+  if (threadIdx.x < 32 && col < H) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += s[i][threadIdx.x];
+    for (int i = 0; i < 32; ++i) t += s[i][threadIdx.x];
     out[col] = t;
   }
 }
 
-// Rows in flight of the backward pass; each leaves one fp32 row of weight
-// gradient sums.
-int norm_grad_groups(int T, int waves) {
-  const int cap = 256 * (16 / waves > 4 ? 4 : 16 / waves > 0 ? 16 / waves : 1);
-  return T < cap ? T : cap;
-}
 int norm_waves(int H, int nv) { return ceil_div(H, kWave * kVec * nv); }
-int norm_grad_nv(int H) {
-  if (norm_waves(H, 1) <= 1) return 1;
-  return norm_waves(H, 2) <= 8 ? 2 : 4;
+
+// The backward pass: vectors per thread, rows per workgroup (about 8 waves
+// where rows are short) and workgroups: 16 waves per CU, as the registers
+// allow; each workgroup leaves one fp32 row of weight gradient sums, and more
+// workgroups than stay resident cost more in those than they hide (8192 x
+// 7168 fp32: 157 / 165 / 170 us with 256 / 512 / 768; 8192 x 4096 bf16 54 /
+// 61 with 512 / 768 of 8 waves).
+struct GradShape {
+  int nv, waves, rows, grid;
+};
+GradShape grad_shape(int T, int H) {
+  GradShape g;
+  g.nv = norm_waves(H, 1) <= 16 ? 1 : norm_waves(H, 2) <= 16 ? 2 : 4;
+  g.waves = norm_waves(H, g.nv);
+  g.rows = g.waves >= 8 ? 1 : 8 / g.waves;
+  const int turns = ceil_div(T, g.rows), fit = 256 * (g.waves > 8 ? 1 : 2);
+  g.grid = turns < fit ? turns : fit;
+  return g;
 }
 
 template <int NV>
-void launch_grad_nv(const NormGradP& p, int h_fp32, int grid, int threads, hipStream_t s) {
+void launch_grad_nv(const NormGradP& p, int h_fp32, const GradShape& g, hipStream_t s) {
+  const int threads = g.rows * g.waves * kWave;
+  const size_t lds = g.rows > 1 ? (size_t)threads * NV * kVec * sizeof(float) : 0;
   if (h_fp32)
-    norm_grad_kernel<NV, true><<<grid, threads, 0, s>>>(p);
+    norm_grad_kernel<NV, true><<<g.grid, threads, lds, s>>>(p);
   else
-    norm_grad_kernel<NV, false><<<grid, threads, 0, s>>>(p);
+    norm_grad_kernel<NV, false><<<g.grid, threads, lds, s>>>(p);
 }
 
 moe_status norm_shape(int T, int H, float eps) {
@@ -398,10 +524,18 @@ moe_status launch_norm(const void* x, const void* residual, int residual_is_fp32
   p.eps = eps;
   p.inv_h = 1.f / (float)H;
   p.w_fp32 = weight_is_fp32;
-  const int nv = norm_waves(H, 1) <= 16 && T < 256 ? 1 : norm_waves(H, 2) <= 8 ? 2 : 4;
+  // One vector per thread up to 8192 columns, two where rows are short and
+  // many; about 8 waves per workgroup.  Measured (bf16, us): 8192 x 4096 with
+  // MX codes 59.8 / 62.9 / 68.1 with 1 / 2 / 4 vectors, 8192 x 1024 12.9 /
+  // 11.9 / 14.5, 1 x 7168 with fp8 codes 4.7 / 4.9 / 5.8.
+  int nv = norm_waves(H, 1) <= 16 ? 1 : norm_waves(H, 2) <= 16 ? 2 : 4;
+  if (H <= 2048 && H > 512 && T >= 4096) nv = 2;
   p.waves = norm_waves(H, nv);
-  if (p.waves == 3) p.waves = 4;  // rows of a workgroup: 4 / waves
-  const int rows = p.waves >= 4 ? 1 : 4 / p.waves;
+  const int rows = p.waves >= 8 ? 1 : 8 / p.waves;
+  // h and y of more than 64 MiB do not stay in the caches until the next
+  // kernel reads them: stored with the non-temporal hint (8192 x 4096 with MX
+  // codes 58.8 -> 54.9 us, 8192 x 7168 with an fp32 residual 142 -> 139)
+  p.once = (uint64_t)T * H * (2 + (!residual ? 0 : residual_is_fp32 ? 4 : 2)) > (64ull << 20);
   const dim3 grid((unsigned)ceil_div(T, rows));
   if ((uint64_t)grid.x * rows * p.waves * kWave > 0xFFFFFFFFull) return MOE_E_UNSUPPORTED;  // HIP's limit of a grid
   const int threads = rows * p.waves * kWave, rt = !residual ? 0 : residual_is_fp32 ? 2 : 1;
@@ -428,8 +562,7 @@ extern "C" moe_status moe_rms_norm(const void* x, const void* residual, int resi
 
 extern "C" size_t moe_rms_norm_grad_workspace_size(int T, int H) {
   if (T < 0 || H < 1 || H > moe::kMaxNormH) return 0;
-  const int waves = moe::norm_waves(H, moe::norm_grad_nv(H));
-  return moe::kCtrlBytes + moe::align_up((size_t)moe::norm_grad_groups(T, waves) * H * sizeof(float), 256);
+  return moe::kCtrlBytes + moe::align_up((size_t)moe::grad_shape(T, H).grid * H * sizeof(float), 256);
 }
 
 extern "C" moe_status moe_rms_norm_grad(const void* dy, const void* dh, const void* h, int h_is_fp32,
@@ -445,7 +578,7 @@ extern "C" moe_status moe_rms_norm_grad(const void* dy, const void* dh, const vo
     if (!workspace) return MOE_E_INVAL;
     if (workspace_bytes < moe_rms_norm_grad_workspace_size(T, H)) return MOE_E_WORKSPACE;
   }
-  const int nv = norm_grad_nv(H), waves = norm_waves(H, nv), grid = norm_grad_groups(T, waves);
+  const GradShape g = grad_shape(T, H);
   NormGradP p;
   p.dy = static_cast<const uint16_t*>(dy);
   p.dh = dh;
@@ -458,16 +591,17 @@ extern "C" moe_status moe_rms_norm_grad(const void* dy, const void* dh, const vo
   p.eps = eps;
   p.inv_h = 1.f / (float)H;
   p.w_fp32 = weight_is_fp32;
+  p.waves = g.waves;
   if (T > 0) {
-    switch (nv) {
-      case 1: launch_grad_nv<1>(p, h_is_fp32, grid, waves * kWave, stream); break;
-      case 2: launch_grad_nv<2>(p, h_is_fp32, grid, waves * kWave, stream); break;
-      default: launch_grad_nv<4>(p, h_is_fp32, grid, waves * kWave, stream); break;
+    switch (g.nv) {
+      case 1: launch_grad_nv<1>(p, h_is_fp32, g, stream); break;
+      case 2: launch_grad_nv<2>(p, h_is_fp32, g, stream); break;
+      default: launch_grad_nv<4>(p, h_is_fp32, g, stream); break;
     }
     MOE_CHECK_LAUNCH();
   }
   if (d_weight) {
-    column_sum_kernel<<<ceil_div(H, 64), 256, 0, stream>>>(p.part, grid, H, d_weight);
+    column_sum_kernel<<<ceil_div(H, 32), 256, 0, stream>>>(p.part, T > 0 ? g.grid : 0, H, d_weight);
     MOE_CHECK_LAUNCH();
   }
   return MOE_OK;
