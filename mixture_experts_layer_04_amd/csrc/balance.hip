@@ -321,29 +321,32 @@ __global__ __launch_bounds__(NT) void balance_kernel(BalanceP p) {
   }
 }
 
-// Grid (sequences, Ep / 64), 1024 threads: adds the pieces of a sequence for
-// 64 experts (64 slices of the pieces, then the slices), writes its counts
-// and mean probabilities, and this tile's share of sum_e c P.
-__global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceP p) {
-  __shared__ float ps[64][64];
-  __shared__ int32_t cs[64][64];
-  __shared__ float zs[16];
-  __shared__ int ns[16];
-  const int s = blockIdx.x, wave = threadIdx.x >> 6;
+// Adds the pieces of sequence s for the 64 experts of a tile (NT / 16 slices
+// of the pieces, then the slices) and writes its counts and mean
+// probabilities; in wave 0, dot: the tile's share of sum_e (E c / (k n)) P.
+template <int NT>
+struct SeqSums {
+  float ps[NT / 16][64];
+  int32_t cs[NT / 16][64];
+  float zs[NT / kWave];
+  int ns[NT / kWave];
+};
+template <int NT>
+__device__ __forceinline__ void add_pieces(const BalanceP& p, SeqSums<NT>& sh, int s, int tile, float& dot, float& z,
+                                           int& n) {
   const int lo = p.off ? seq_at(p.off, s, p.T) : 0, hi = p.off ? seq_at(p.off, s + 1, p.T) : p.T;
   const int first = lo / p.chunk, last = hi > lo ? (hi - 1) / p.chunk : first - 1;
   const int quad = threadIdx.x & 15, slice = threadIdx.x >> 4;
-  const int e0 = blockIdx.y * 64;
   f32x4_t pa = {0.f, 0.f, 0.f, 0.f};
   i32x4_t ca = {0, 0, 0, 0};
-  for (int c = first + slice; c <= last; c += 64) {
-    const size_t at = (size_t)(c + s) * p.Ep + e0 + quad * 4;
+  for (int c = first + slice; c <= last; c += NT / 16) {
+    const size_t at = (size_t)(c + s) * p.Ep + tile * 64 + quad * 4;
     pa += *reinterpret_cast<const f32x4_t*>(p.psum + at);
     ca += *reinterpret_cast<const i32x4_t*>(p.csum + at);
   }
-  float z = 0.f;
-  int n = 0;
-  for (int c = first + (int)threadIdx.x; c <= last; c += 1024) {
+  z = 0.f;
+  n = 0;
+  for (int c = first + (int)threadIdx.x; c <= last; c += NT) {
     z += p.zsum[c + s];
     n += p.nsum[c + s];
   }
@@ -351,82 +354,99 @@ __global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceP p) {
 #pragma unroll
   for (int off = 32; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
   if ((threadIdx.x & 63) == 0) {
-    zs[wave] = z;
-    ns[wave] = n;
+    sh.zs[threadIdx.x >> 6] = z;
+    sh.ns[threadIdx.x >> 6] = n;
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    ps[slice][quad * 4 + i] = pa[i];
-    cs[slice][quad * 4 + i] = ca[i];
+    sh.ps[slice][quad * 4 + i] = pa[i];
+    sh.cs[slice][quad * 4 + i] = ca[i];
   }
   __syncthreads();
+  dot = 0.f;
   if (threadIdx.x < 64) {
     n = 0;
     z = 0.f;
-    for (int i = 0; i < 16; ++i) {
-      n += ns[i];
-      z += zs[i];
+    for (int i = 0; i < NT / kWave; ++i) {
+      n += sh.ns[i];
+      z += sh.zs[i];
     }
     float P = 0.f;
     int c = 0;
 #pragma unroll 8
-    for (int i = 0; i < 64; ++i) {
-      P += ps[i][threadIdx.x];
-      c += cs[i][threadIdx.x];
+    for (int i = 0; i < NT / 16; ++i) {
+      P += sh.ps[i][threadIdx.x];
+      c += sh.cs[i][threadIdx.x];
     }
     P = n > 0 ? P / (float)n : 0.f;
-    const int e = e0 + threadIdx.x;
+    const int e = tile * 64 + threadIdx.x;
     if (e < p.E) {
       p.probs[(size_t)s * p.E + e] = P;
       p.counts[(size_t)s * p.E + e] = c;
     }
-    const float f = n > 0 ? (float)c / (float)n * ((float)p.E / (float)p.k) : 0.f;
-    const float d = wave_sum(f * P);
-    if (threadIdx.x == 0) {
-      p.dot[(size_t)s * gridDim.y + blockIdx.y] = d;
-      if (blockIdx.y == 0) {
-        p.zseq[s] = z;
-        p.nseq[s] = n;
-      }
-    }
+    dot = wave_sum(n > 0 ? (float)c / (float)n * ((float)p.E / (float)p.k) * P : 0.f);
   }
 }
 
-// One workgroup: the losses from the sequences' shares, and the token and
-// sequence numbers behind the per-sequence ones.
-__global__ __launch_bounds__(256) void balance_total_kernel(BalanceP p, int tiles) {
-  __shared__ double bs[256], zs[256];
-  __shared__ int ns[256], fs[256];
-  double b = 0.0, z = 0.0;
-  int n = 0, full = 0;
-  for (int s = threadIdx.x; s < p.S; s += 256) {
-    for (int i = 0; i < tiles; ++i) b += (double)p.dot[(size_t)s * tiles + i];
-    z += (double)p.zseq[s];
-    n += p.nseq[s];
-    full += p.nseq[s] > 0;
+// The sums over the sequences (in 64 bits), and what the losses are of them.
+struct Totals {
+  double b, z;
+  int n, full;
+  __device__ __forceinline__ void write(const BalanceP& p) const {
+    p.losses[0] = full ? (float)(b / full) : 0.f;
+    p.losses[1] = n ? (float)(z / n) : 0.f;
+    p.nseq[p.S] = n;
+    p.nseq[p.S + 1] = full;
   }
-  bs[threadIdx.x] = b;
-  zs[threadIdx.x] = z;
-  ns[threadIdx.x] = n;
-  fs[threadIdx.x] = full;
-  __syncthreads();
-  for (int w = 128; w >= 1; w >>= 1) {
-    if ((int)threadIdx.x < w) {
-      bs[threadIdx.x] += bs[threadIdx.x + w];
-      zs[threadIdx.x] += zs[threadIdx.x + w];
-      ns[threadIdx.x] += ns[threadIdx.x + w];
-      fs[threadIdx.x] += fs[threadIdx.x + w];
-    }
-    __syncthreads();
-  }
+};
+
+// Grid (sequences, tiles), and then one workgroup for the totals.  Slower:
+// totals by the workgroup that arrives last, instead of a launch of their own
+// (every arrival is an L2 write-back, 10.3 against 4.8 + 3.5 us at 37
+// sequences of 256 experts), and one workgroup for all of it in small batches
+// (about 4 us a tile: 23 against 14 us at 4096 x 256).
+template <int NT>
+__global__ __launch_bounds__(NT) void balance_seq_kernel(BalanceP p) {
+  __shared__ SeqSums<NT> sh;
+  float dot, z;
+  int n;
+  add_pieces<NT>(p, sh, blockIdx.x, blockIdx.y, dot, z, n);
   if (threadIdx.x == 0) {
-    p.losses[0] = fs[0] ? (float)(bs[0] / fs[0]) : 0.f;
-    p.losses[1] = ns[0] ? (float)(zs[0] / ns[0]) : 0.f;
-    p.nseq[p.S] = ns[0];
-    p.nseq[p.S + 1] = fs[0];
+    p.dot[(size_t)blockIdx.x * gridDim.y + blockIdx.y] = dot;
+    if (blockIdx.y == 0) {
+      p.zseq[blockIdx.x] = z;
+      p.nseq[blockIdx.x] = n;
+    }
   }
 }
-
+__global__ __launch_bounds__(256) void balance_total_kernel(BalanceP p, int tiles) {
+  __shared__ Totals sh[4];
+  Totals a = {0.0, 0.0, 0, 0};
+  for (int s = threadIdx.x; s < p.S; s += 256) {
+    for (int i = 0; i < tiles; ++i) a.b += (double)p.dot[(size_t)s * tiles + i];
+    a.z += (double)p.zseq[s];
+    a.n += p.nseq[s];
+    a.full += p.nseq[s] > 0;
+  }
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) {
+    a.b += __shfl_xor(a.b, off, kWave);
+    a.z += __shfl_xor(a.z, off, kWave);
+    a.n += __shfl_xor(a.n, off, kWave);
+    a.full += __shfl_xor(a.full, off, kWave);
+  }
+  if ((threadIdx.x & 63) == 0) sh[threadIdx.x >> 6] = a;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 4; ++w) {
+      a.b += sh[w].b;
+      a.z += sh[w].z;
+      a.n += sh[w].n;
+      a.full += sh[w].full;
+    }
+    a.write(p);
+  }
+}
 struct RouteGradP {
   const float* logits;
   const int32_t* ids;
@@ -660,8 +680,10 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradP p) {
   }
 }
 
-// Rows per workgroup of the loss: at most 1024 chunks, none below 16 rows.
-int balance_chunk(int T) { return T <= 16 * 1024 ? 16 : ceil_div(ceil_div(T, 1024), 16) * 16; }
+// Rows per workgroup of the loss, a multiple of 16: at most 512 chunks, 1024
+// in large batches (65536 x 64: 17.9 / 20.1 us with 512 / 1024; 131072 x 256:
+// 39.2 / 37.1).
+int balance_chunk(int T) { return ceil_div(T > 0 ? T : 1, 16 * (T <= 65536 ? 512 : 1024)) * 16; }
 
 struct BalanceLayout {
   size_t psum, csum, zsum, nsum, dot, zseq, total;
@@ -720,10 +742,12 @@ void balance_launch(const BalanceP& p, bool one, int scoring, hipStream_t s) {
 }
 template <int LANES, int NV>
 void route_grad_launch(RouteGradP p, int scoring, hipStream_t s) {
-  // one token per lane group until the chip is full, then up to four
+  // one token per lane group until the chip is full, then three, with the
+  // next one's loads under way (us with 1 / 2 / 3 / 4: 16384 x 128 7.0 / 7.4 /
+  // 8.7 / 9.4, 65536 x 128 17.1 / 17.1 / 15.8 / 16.0, 131072 x 256 68.5 /
+  // 61.5 / 61.7 / 62.1)
   constexpr int GROUPS = 256 / LANES;
-  const int64_t runs = ceil_div64(p.T, GROUPS);
-  p.rows = GROUPS * (int)(runs <= 1024 ? 1 : runs >= 4096 ? 4 : ceil_div64(runs, 1024));
+  p.rows = GROUPS * (ceil_div64(p.T, GROUPS) <= 2048 ? 1 : 3);
   const int grid = ceil_div(p.T, p.rows);
   switch (scoring) {
     case MOE_SOFTMAX: route_grad_kernel<LANES, NV, MOE_SOFTMAX><<<grid, 256, 0, s>>>(p); break;
@@ -805,7 +829,10 @@ extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_
   }
   if (one) return MOE_OK;
   const dim3 grid((unsigned)n_seq, (unsigned)(p.Ep / 64));
-  balance_seq_kernel<<<grid, 1024, 0, stream>>>(p);
+  if (p.chunks / n_seq > 64)  // pieces of an average sequence
+    balance_seq_kernel<1024><<<grid, 1024, 0, stream>>>(p);
+  else
+    balance_seq_kernel<256><<<grid, 256, 0, stream>>>(p);
   MOE_CHECK_LAUNCH();
   balance_total_kernel<<<1, 256, 0, stream>>>(p, p.Ep / 64);
   MOE_CHECK_LAUNCH();

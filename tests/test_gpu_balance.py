@@ -382,3 +382,23 @@ def test_refusals():
     for f in errors:
         with pytest.raises(moe.MoeError):
             f()
+
+
+def test_many_sequences():
+    """More sequences than one launch totals by its last workgroup, most of
+    them one or two tokens long or empty."""
+    import mixture_experts_layer_04_amd as moe
+    T, E, k = 700, 40, 4
+    lg, ids = make(T, E, k)
+    rng = np.random.default_rng(3)
+    off = np.sort(rng.integers(0, T + 1, size=1500)).tolist()
+    offd, _ = to_dev(off, None)
+    got = moe.balance_loss(lg, ids, "sigmoid", offd)
+    d = moe.route_grad(lg, ids, "sigmoid", d_losses=torch.tensor([900.0, 30.0], device="cuda"), counts=got[1],
+                       tokens=got[3], seq_offsets=offd)
+    torch.cuda.synchronize()
+    ref = ob.balance_loss(f64(lg), ids.cpu().numpy(), "sigmoid", off)
+    check_loss(got, ref, lg, ob.members(T, off)[0])
+    want, mag = ob.route_grad(f64(lg), ids.cpu().numpy(), "sigmoid", True, 1.0, None, np.array([900.0, 30.0]),
+                              ref["counts"], off)
+    assert np.all(np.abs(f64(d) - want) <= mag * 2.0 ** -15 + 1e-35)
