@@ -1,6 +1,8 @@
 /*
  * moe.h - C ABI of libmoe, a single-GPU Mixture-of-Experts layer forward for
- * AMD Instinct MI355X (gfx950).
+ * AMD Instinct MI355X (gfx950), with the norm in front of the layer (and its
+ * gradient) and the router's training side: balance and z losses, and the
+ * gradients to the logits, the gate and the hidden states.
  *
  * The layer is: router (gate logits, scoring, selection bias, optional group
  * limit, top-k, renormalisation) -> block alignment (per-expert histogram,
@@ -387,7 +389,7 @@ int moe_layer_block_m(int T, int E, int F, int k, int wformat);
  * is an fp32 value, so a row whose sum of squares passes 3.4e38 gives zeros
  * (and NaN where h is infinite).
  * x, residual, weight, h and y need the alignment of an element only, s
- * too; q 8 bytes.  No workspace.  Constraints: 0 <= T <= 2^24, 1 <= H;
+ * too; q 8 bytes (else MOE_E_INVAL).  No workspace.  Constraints: 0 <= T <= 2^24, 1 <= H;
  * H > 32768, or an H that the format's group does not divide:
  * MOE_E_UNSUPPORTED.
  * ------------------------------------------------------------------------ */
@@ -530,7 +532,8 @@ moe_status moe_route_grad(const float* logits, const int32_t* topk_ids,
  * 2^-15 of each product.  T = 0 writes a zero d_gate.  An operand that is
  * not finite makes the rows it meets not finite (an infinity may become a
  * NaN).  Constraints: 0 <= T <= 2^24, H a multiple of 128 and at most 2^20,
- * 1 <= E <= 1024.
+ * 1 <= E <= 1024; every pointer but d_logits 16-byte aligned, else
+ * MOE_E_INVAL.
  * ------------------------------------------------------------------------ */
 moe_status moe_gate_grad(const void* x, const void* gate, int gate_is_fp32,
                          const float* d_logits, const void* dx_in, int T, int H, int E,

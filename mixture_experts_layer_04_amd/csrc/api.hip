@@ -234,7 +234,7 @@ extern "C" moe_status moe_norm_layer(const void* x, const void* residual, int re
                                      void* y, int32_t* topk_ids_out, float* topk_weights_out, void* workspace,
                                      size_t workspace_bytes, hipStream_t stream) {
   using namespace moe;
-  uint8_t dummy = 0;
+  alignas(16) uint8_t dummy = 0;
   moe_status st = layer_validate(x, gate, gate_is_fp32, wformat, w13, w13_scale, w2, w2_scale, T, H, E, F, k, n_shared,
                                  n_group, topk_group, scoring, block_m, swiglu_limit, y);
   if (st != MOE_OK) return st;

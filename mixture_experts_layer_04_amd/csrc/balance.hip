@@ -792,7 +792,7 @@ extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_
   if (T > 0 && (!logits || !topk_ids)) return MOE_E_INVAL;
   if (!losses || !counts || !probs || !tokens) return MOE_E_INVAL;
   const BalanceLayout L = balance_layout(T, E, n_seq);
-  if (L.total > 0 && !workspace) return MOE_E_INVAL;
+  if (L.total > 0 && (!workspace || !aligned(workspace, 16))) return MOE_E_INVAL;
   if (workspace_bytes < L.total) return MOE_E_WORKSPACE;
   char* b = static_cast<char*>(workspace);
   BalanceP p;

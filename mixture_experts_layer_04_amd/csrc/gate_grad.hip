@@ -742,6 +742,8 @@ extern "C" moe_status moe_gate_grad(const void* x, const void* gate, int gate_is
   if (!gate_grad_shape(T, H, E) || gate_is_fp32 < 0 || gate_is_fp32 > 1) return MOE_E_INVAL;
   if (!dx && !d_gate) return MOE_E_INVAL;
   if (dx_in && !dx) return MOE_E_INVAL;
+  for (const void* q : {x, gate, dx_in, (const void*)dx, (const void*)d_gate, (const void*)workspace})
+    if (!aligned(q, 16)) return MOE_E_INVAL;
   const size_t len4 = (size_t)E * H / 4;
   if (T == 0) {
     if (!d_gate) return MOE_OK;

@@ -109,6 +109,10 @@ moe_status launch_gemm_mxfp4(const FfnArgs& a, int which, hipStream_t stream);
 moe_status launch_quant_x(const FfnArgs& a, hipStream_t stream);
 moe_status launch_finalize(const FfnArgs& a, hipStream_t stream);
 
+// Whether a pointer (null too) has the alignment that a kernel's vector
+// accesses need.
+inline bool aligned(const void* p, uintptr_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
+
 // The norm in front of the layer (norm.hip): qformat is the moe_wformat whose
 // activation format q / s take (MOE_W_BF16: none).
 moe_status norm_validate(const void* x, const void* residual, int residual_is_fp32, const void* weight,

@@ -501,6 +501,7 @@ moe_status norm_validate(const void* x, const void* residual, int residual_is_fp
   if (residual_is_fp32 < 0 || residual_is_fp32 > 1 || weight_is_fp32 < 0 || weight_is_fp32 > 1) return MOE_E_INVAL;
   if (qformat != MOE_W_BF16 && qformat != MOE_W_FP8_BLOCK128 && qformat != MOE_W_MXFP4) return MOE_E_INVAL;
   if (h && !residual) return MOE_E_INVAL;
+  if (qformat != MOE_W_BF16 && !aligned(q, 8)) return MOE_E_INVAL;
   if ((qformat == MOE_W_FP8_BLOCK128 && H % 128) || (qformat == MOE_W_MXFP4 && H % 32)) return MOE_E_UNSUPPORTED;
   if (T == 0) return MOE_OK;
   if (!x || !weight) return MOE_E_INVAL;

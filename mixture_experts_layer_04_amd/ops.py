@@ -236,18 +236,25 @@ _RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 _TYPE_IS_FP32 = {torch.float32: 1, torch.bfloat16: 0}
 
 
-def _tensor(name, t, dtypes, shape, device):
-    """Checks one argument (a dtype or a tuple of them; the shape)."""
-    if t.dtype == dtypes and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+def _tensor(name, t, dtype, shape, device):
+    """Checks one argument: its type, shape, device and layout."""
+    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
         return
     if not t.is_cuda or t.device != device:
         raise ValueError(f"{name}: libmoe ops take GPU tensors of one device, not {t.device}")
-    if t.dtype != dtypes and not (isinstance(dtypes, tuple) and t.dtype in dtypes):
-        raise ValueError(f"{name} has type {t.dtype}, not {dtypes}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has type {t.dtype}, not {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: libmoe ops take contiguous tensors")
+    raise ValueError(f"{name}: libmoe ops take contiguous tensors")
+
+
+def _is_fp32(name, t):
+    """1 for a float32 tensor, 0 for a bfloat16 one."""
+    f = _TYPE_IS_FP32.get(t.dtype)
+    if f is None:
+        raise ValueError(f"{name} is float32 or bfloat16, not {t.dtype}")
+    return f
 
 
 def _call(name, device, *args):
@@ -259,9 +266,6 @@ def _call(name, device, *args):
             check(fn(*args, _raw_stream(device.index)), name)
     else:
         check(fn(*args, _raw_stream(device.index)), name)
-
-
-_BF16_FP32 = (torch.bfloat16, torch.float32)
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=None, s=None, with_y=True):
@@ -278,13 +282,14 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=N
     T, H = x.shape
     dev = x.device
     _tensor("x", x, torch.bfloat16, (T, H), dev)
-    _tensor("weight", weight, _BF16_FP32, (H,), dev)
+    wf = _is_fp32("weight", weight)
+    _tensor("weight", weight, weight.dtype, (H,), dev)
     if quant not in (None, "fp8", "mxfp4"):
         raise ValueError(f"quant is None, 'fp8' or 'mxfp4', not {quant!r}")
     rf = 0
     if residual is not None:
-        _tensor("residual", residual, _BF16_FP32, (T, H), dev)
-        rf = _TYPE_IS_FP32[residual.dtype]
+        rf = _is_fp32("residual", residual)
+        _tensor("residual", residual, residual.dtype, (T, H), dev)
         if h is None:
             h = torch.empty_like(residual)
         else:
@@ -312,8 +317,8 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=N
             s = torch.empty((T, H // group), dtype=st, device=dev)
         else:
             _tensor("s", s, st, (T, H // group), dev)
-    _call("moe_rms_norm", dev, x.data_ptr(), _ptr(residual), rf, weight.data_ptr(), _TYPE_IS_FP32[weight.dtype], T, H,
-          eps, qf, _ptr(h), _ptr(y), _ptr(q), _ptr(s))
+    _call("moe_rms_norm", dev, x.data_ptr(), _ptr(residual), rf, weight.data_ptr(), wf, T, H, eps, qf,
+          _ptr(h), _ptr(y), _ptr(q), _ptr(s))
     return (y, h) if quant is None else (y, h, q, s)
 
 
@@ -327,8 +332,9 @@ def rms_norm_grad(dy, h, weight, eps=1e-6, dh=None, dx=None, with_weight=True):
     T, H = dy.shape
     dev = dy.device
     _tensor("dy", dy, torch.bfloat16, (T, H), dev)
-    _tensor("h", h, _BF16_FP32, (T, H), dev)
-    _tensor("weight", weight, _BF16_FP32, (H,), dev)
+    hf, wf = _is_fp32("h", h), _is_fp32("weight", weight)
+    _tensor("h", h, h.dtype, (T, H), dev)
+    _tensor("weight", weight, weight.dtype, (H,), dev)
     if dh is not None:
         _tensor("dh", dh, h.dtype, (T, H), dev)
     if dx is None:
@@ -341,8 +347,8 @@ def rms_norm_grad(dy, h, weight, eps=1e-6, dh=None, dx=None, with_weight=True):
         dw = torch.empty(H, dtype=torch.float32, device=dev)
         need = lib().moe_rms_norm_grad_workspace_size(T, H)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call("moe_rms_norm_grad", dev, dy.data_ptr(), _ptr(dh), h.data_ptr(), _TYPE_IS_FP32[h.dtype], weight.data_ptr(),
-          _TYPE_IS_FP32[weight.dtype], T, H, eps, dx.data_ptr(), _ptr(dw), _ptr(ws), need)
+    _call("moe_rms_norm_grad", dev, dy.data_ptr(), _ptr(dh), h.data_ptr(), hf, weight.data_ptr(), wf, T, H, eps,
+          dx.data_ptr(), _ptr(dw), _ptr(ws), need)
     return dx, dw
 
 
@@ -361,7 +367,7 @@ def _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask):
         n_seq = seq_offsets.shape[0] - 1
         _tensor("seq_offsets", seq_offsets, torch.int32, (n_seq + 1,), dev)
     if token_mask is not None:
-        _tensor("token_mask", token_mask, (torch.uint8, torch.bool), (T,), dev)
+        _tensor("token_mask", token_mask, torch.bool if token_mask.dtype == torch.bool else torch.uint8, (T,), dev)
     return T, E, topk_ids.shape[1] - n_shared, n_seq
 
 
@@ -424,7 +430,8 @@ def gate_grad(x, gate, d_logits, dx_in=None, dx=None, with_dx=True, with_gate=Tr
     E = gate.shape[0]
     dev = x.device
     _tensor("x", x, torch.bfloat16, (T, H), dev)
-    _tensor("gate", gate, _BF16_FP32, (E, H), dev)
+    gf = _is_fp32("gate", gate)
+    _tensor("gate", gate, gate.dtype, (E, H), dev)
     _tensor("d_logits", d_logits, torch.float32, (T, E), dev)
     if not with_dx and (dx is not None or dx_in is not None):
         raise ValueError("dx and dx_in without with_dx")
@@ -437,8 +444,8 @@ def gate_grad(x, gate, d_logits, dx_in=None, dx=None, with_dx=True, with_gate=Tr
     d_gate = torch.empty((E, H), dtype=torch.float32, device=dev) if with_gate else None
     need = lib().moe_gate_grad_workspace_size(T, H, E)
     ws = torch.empty(need, dtype=torch.uint8, device=dev)
-    _call("moe_gate_grad", dev, x.data_ptr(), gate.data_ptr(), _TYPE_IS_FP32[gate.dtype], d_logits.data_ptr(),
-          _ptr(dx_in), T, H, E, _ptr(dx), _ptr(d_gate), ws.data_ptr(), need)
+    _call("moe_gate_grad", dev, x.data_ptr(), gate.data_ptr(), gf, d_logits.data_ptr(), _ptr(dx_in), T, H, E,
+          _ptr(dx), _ptr(d_gate), ws.data_ptr(), need)
     return dx, d_gate
 
 
@@ -459,11 +466,12 @@ def norm_layer(x, norm_weight, gate, bias, w13, w2, k, residual=None, eps=1e-6, 
     if Ew != E + n_shared:
         raise ValueError(f"w13 holds {Ew} experts, the gate {E} and n_shared = {n_shared}")
     _tensor("x", x, torch.bfloat16, (T, H), dev)
-    _tensor("norm_weight", norm_weight, _BF16_FP32, (H,), dev)
+    nf = _is_fp32("norm_weight", norm_weight)
+    _tensor("norm_weight", norm_weight, norm_weight.dtype, (H,), dev)
     rf = 0
     if residual is not None:
-        _tensor("residual", residual, _BF16_FP32, (T, H), dev)
-        rf = _TYPE_IS_FP32[residual.dtype]
+        rf = _is_fp32("residual", residual)
+        _tensor("residual", residual, residual.dtype, (T, H), dev)
         if h is None:
             h = torch.empty_like(residual)
         else:
@@ -480,8 +488,8 @@ def norm_layer(x, norm_weight, gate, bias, w13, w2, k, residual=None, eps=1e-6, 
     wf = WFORMAT[wformat]
     need = lib().moe_norm_layer_workspace_size(T, H, E, F, k, n_shared, block_m, wf)
     ws = workspace(dev, need) if ws is None else ws
-    _call("moe_norm_layer", dev, x.data_ptr(), _ptr(residual), rf, norm_weight.data_ptr(),
-          _TYPE_IS_FP32[norm_weight.dtype], eps, _ptr(gate), _gate_is_fp32(gate), _ptr(bias), wf, _ptr(w13),
+    _call("moe_norm_layer", dev, x.data_ptr(), _ptr(residual), rf, norm_weight.data_ptr(), nf, eps,
+          _ptr(gate), _gate_is_fp32(gate), _ptr(bias), wf, _ptr(w13),
           _ptr(w13_scale), _ptr(w2), _ptr(w2_scale), T, H, E, F, k, n_shared, n_group, topk_group, SCORING[scoring],
           int(bool(renormalize)), float(routed_scale), block_m, float(swiglu_limit), _ptr(h), _ptr(y), _ptr(ids),
           _ptr(w), _ptr(ws), ws.numel())

@@ -32,6 +32,7 @@ def test_rms_norm(L):
     assert call(x=None) == INVAL and call(w=None) == INVAL and call(y=None) == INVAL
     assert call(res=None) == INVAL                      # h without a residual
     assert call(q=1, qo=None, s=FAKE) == INVAL and call(q=2, qo=FAKE, s=None) == INVAL
+    assert call(q=1, qo=ctypes.c_void_p(0x1004), s=FAKE) == INVAL  # q is 8-byte aligned
     assert call(H=32769) == UNSUPPORTED
     assert call(q=1, H=192, qo=FAKE, s=FAKE) == UNSUPPORTED and call(q=2, H=48, qo=FAKE, s=FAKE) == UNSUPPORTED
 
@@ -78,6 +79,8 @@ def test_gate_grad(L):
     assert call(T=-1) == INVAL and call(H=100) == INVAL and call(H=0) == INVAL and call(E=1025) == INVAL
     assert call(gf=2) == INVAL and call(dx=None, dg=None) == INVAL and call(dx=None, di=FAKE) == INVAL
     assert call(d=None) == INVAL and call(x=None) == INVAL and call(g=None) == INVAL and call(ws=None) == INVAL
+    odd = ctypes.c_void_p(0x1008)  # 8-byte aligned only
+    assert call(x=odd) == INVAL and call(dx=odd) == INVAL and call(di=odd) == INVAL and call(ws=odd) == INVAL
     assert call(n=70000) == WORKSPACE and call(T=0, dg=None) == OK
     assert L.moe_gate_grad_workspace_size(4, 100, 8) == 0
 
