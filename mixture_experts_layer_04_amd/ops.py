@@ -18,7 +18,7 @@ import math
 
 import torch
 
-from ._lib import SCORING, STAGE, WFORMAT, check, lib
+from ._lib import SCORING, STAGE, WFORMAT, MoeError, check, lib
 
 _WS = {}
 # Workspaces the cache has outgrown.  They are never freed: a HIP graph
@@ -226,27 +226,36 @@ def layer_noalloc(x, gate, bias, w13, w2, k, scoring="softmax", n_group=1, topk_
 # ---------------------------------------------------------------------------
 # the norm in front of the layer, and the router's training side
 
-def _raw_stream(index):
-    """The current stream's handle.  torch._C's query takes 0.1 us, building a
-    torch.cuda.Stream for it 1.9 us, a fifth of a decode-sized call."""
-    return _RAW_STREAM(index) if _RAW_STREAM else torch.cuda.current_stream(index).cuda_stream
-
-
-_RAW_STREAM = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+# A decode-sized call is mostly host time, so what every call asks of torch
+# goes the short way: these queries of torch._C take 0.1 us each, building a
+# torch.cuda.Stream for its handle 1.9 us.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda index: torch.cuda.current_stream(index).cuda_stream)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _TYPE_IS_FP32 = {torch.float32: 1, torch.bfloat16: 0}
 
 
-def _tensor(name, t, dtype, shape, device):
-    """Checks one argument: its type, shape, device and layout."""
-    if t.dtype == dtype and t.shape == shape and t.device == device and t.is_cuda and t.is_contiguous():
+def _tensor(name, t, dtype, shape, index):
+    """Checks one argument: its type, shape, device (by its index) and
+    layout."""
+    if t.dtype == dtype and t.shape == shape and t.get_device() == index and t.is_contiguous():
         return
-    if not t.is_cuda or t.device != device:
+    if not t.is_cuda or t.get_device() != index:
         raise ValueError(f"{name}: libmoe ops take GPU tensors of one device, not {t.device}")
     if t.dtype != dtype:
         raise ValueError(f"{name} has type {t.dtype}, not {dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     raise ValueError(f"{name}: libmoe ops take contiguous tensors")
+
+
+def _gpu(name, t, dims):
+    """The device index of a call's first argument, a GPU tensor of ``dims``
+    dimensions."""
+    if not t.is_cuda:
+        raise ValueError(f"{name}: libmoe ops take GPU tensors, not {t.device}")
+    if t.dim() != dims:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {dims} dimensions")
+    return t.get_device()
 
 
 def _is_fp32(name, t):
@@ -257,15 +266,17 @@ def _is_fp32(name, t):
     return f
 
 
-def _call(name, device, *args):
-    """One library call on the current stream of ``device``, with that
-    device current while the kernels are launched."""
+def _call(name, index, *args):
+    """One library call on the current stream of a device, with that device
+    current while the kernels are launched."""
     fn = getattr(lib(), name)
-    if torch.cuda.current_device() != device.index:
-        with torch.cuda.device(device):
-            check(fn(*args, _raw_stream(device.index)), name)
+    if _current_device() == index:
+        status = fn(*args, _raw_stream(index))
     else:
-        check(fn(*args, _raw_stream(device.index)), name)
+        with torch.cuda.device(index):
+            status = fn(*args, _raw_stream(index))
+    if status:
+        raise MoeError(status, name)
 
 
 def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=None, s=None, with_y=True):
@@ -277,11 +288,10 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=N
     of those expert formats, q uint8 [T, H] (e4m3 codes) and s float32
     [T, H/128] or uint8 [T, H/32] (e8m0).  Outputs are allocated unless
     given; h may be the residual (in place)."""
-    if x.dim() != 2:
-        raise ValueError(f"x has shape {tuple(x.shape)}, not [T, H]")
-    T, H = x.shape
-    dev = x.device
-    _tensor("x", x, torch.bfloat16, (T, H), dev)
+    dev = _gpu("x", x, 2)
+    shape = x.shape
+    T, H = shape
+    _tensor("x", x, torch.bfloat16, shape, dev)
     wf = _is_fp32("weight", weight)
     _tensor("weight", weight, weight.dtype, (H,), dev)
     if quant not in (None, "fp8", "mxfp4"):
@@ -289,15 +299,15 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=N
     rf = 0
     if residual is not None:
         rf = _is_fp32("residual", residual)
-        _tensor("residual", residual, residual.dtype, (T, H), dev)
+        _tensor("residual", residual, residual.dtype, shape, dev)
         if h is None:
             h = torch.empty_like(residual)
         else:
-            _tensor("h", h, residual.dtype, (T, H), dev)
+            _tensor("h", h, residual.dtype, shape, dev)
     elif h is not None:
         raise ValueError("h without a residual is x")
     if y is not None:
-        _tensor("y", y, torch.bfloat16, (T, H), dev)
+        _tensor("y", y, torch.bfloat16, shape, dev)
     elif with_y or quant is None:
         y = torch.empty_like(x)
     if quant is None:
@@ -312,7 +322,7 @@ def rms_norm(x, weight, residual=None, eps=1e-6, quant=None, y=None, h=None, q=N
         if q is None:
             q = torch.empty((T, H), dtype=torch.uint8, device=dev)
         else:
-            _tensor("q", q, torch.uint8, (T, H), dev)
+            _tensor("q", q, torch.uint8, shape, dev)
         if s is None:
             s = torch.empty((T, H // group), dtype=st, device=dev)
         else:
@@ -327,10 +337,8 @@ def rms_norm_grad(dy, h, weight, eps=1e-6, dh=None, dx=None, with_weight=True):
     residual) in h's type and of the weight in float32 (None without
     ``with_weight``).  ``h``: the forward call's h, or its x where it had no
     residual; ``dh``: the gradient that reaches h from elsewhere."""
-    if dy.dim() != 2:
-        raise ValueError(f"dy has shape {tuple(dy.shape)}, not [T, H]")
+    dev = _gpu("dy", dy, 2)
     T, H = dy.shape
-    dev = dy.device
     _tensor("dy", dy, torch.bfloat16, (T, H), dev)
     hf, wf = _is_fp32("h", h), _is_fp32("weight", weight)
     _tensor("h", h, h.dtype, (T, H), dev)
@@ -353,11 +361,11 @@ def rms_norm_grad(dy, h, weight, eps=1e-6, dh=None, dx=None, with_weight=True):
 
 
 def _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask):
-    """Checks what balance_loss and route_grad share; (T, E, k, sequences)."""
-    if logits.dim() != 2 or topk_ids.dim() != 2:
-        raise ValueError("logits are [T, E] and topk_ids [T, k]")
+    """Checks what balance_loss and route_grad share; (T, E, k, sequences,
+    device index)."""
+    dev = _gpu("logits", logits, 2)
+    _gpu("topk_ids", topk_ids, 2)
     T, E = logits.shape
-    dev = logits.device
     _tensor("logits", logits, torch.float32, (T, E), dev)
     _tensor("topk_ids", topk_ids, torch.int32, (T, topk_ids.shape[1]), dev)
     n_seq = 1
@@ -368,7 +376,7 @@ def _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask):
         _tensor("seq_offsets", seq_offsets, torch.int32, (n_seq + 1,), dev)
     if token_mask is not None:
         _tensor("token_mask", token_mask, torch.bool if token_mask.dtype == torch.bool else torch.uint8, (T,), dev)
-    return T, E, topk_ids.shape[1] - n_shared, n_seq
+    return T, E, topk_ids.shape[1] - n_shared, n_seq, dev
 
 
 def balance_loss(logits, topk_ids, scoring="softmax", seq_offsets=None, token_mask=None, n_shared=0):
@@ -378,8 +386,7 @@ def balance_loss(logits, topk_ids, scoring="softmax", seq_offsets=None, token_ma
     ``seq_offsets`` int32 [S + 1] on the GPU cuts the rows into sequences
     (default: all rows are one); ``token_mask`` uint8 or bool [T] leaves out
     the rows where it is 0.  counts and tokens go to route_grad."""
-    T, E, k, S = _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask)
-    dev = logits.device
+    T, E, k, S, dev = _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask)
     losses = torch.empty(2, dtype=torch.float32, device=dev)
     counts = torch.empty((S, E), dtype=torch.int32, device=dev)
     probs = torch.empty((S, E), dtype=torch.float32, device=dev)
@@ -398,8 +405,7 @@ def route_grad(logits, topk_ids, scoring="softmax", renormalize=True, routed_sca
     [T, k], the gradient of the routing weights) and / or ``d_losses``
     (float32 [2] on the GPU, the gradient of balance_loss's losses, with its
     counts and tokens)."""
-    T, E, k, S = _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask)
-    dev = logits.device
+    T, E, k, S, dev = _router_args(logits, topk_ids, n_shared, seq_offsets, token_mask)
     if d_weights is None and d_losses is None:
         raise ValueError("route_grad takes d_weights, d_losses or both")
     if d_weights is not None:
@@ -424,11 +430,10 @@ def gate_grad(x, gate, d_logits, dx_in=None, dx=None, with_dx=True, with_gate=Tr
     """moe_gate_grad -> (dx bf16 [T, H], d_gate float32 [E, H]): dx =
     d_logits gate (+ dx_in), d_gate = d_logits^T x; None for the one that
     is not wanted.  dx may be dx_in (in place)."""
-    if x.dim() != 2 or gate.dim() != 2:
-        raise ValueError("x is [T, H] and the gate [E, H]")
+    dev = _gpu("x", x, 2)
+    _gpu("gate", gate, 2)
     T, H = x.shape
     E = gate.shape[0]
-    dev = x.device
     _tensor("x", x, torch.bfloat16, (T, H), dev)
     gf = _is_fp32("gate", gate)
     _tensor("gate", gate, gate.dtype, (E, H), dev)
@@ -462,7 +467,7 @@ def norm_layer(x, norm_weight, gate, bias, w13, w2, k, residual=None, eps=1e-6, 
     _check_cuda(x, gate, bias, w13, w2, w13_scale, w2_scale, out, ws)
     T, H, Ew, F = _dims(x, w13, w2, wformat)
     E = gate.shape[0]
-    dev = x.device
+    dev = _gpu("x", x, 2)
     if Ew != E + n_shared:
         raise ValueError(f"w13 holds {Ew} experts, the gate {E} and n_shared = {n_shared}")
     _tensor("x", x, torch.bfloat16, (T, H), dev)
