@@ -529,7 +529,7 @@ moe_status moe_route_grad(const float* logits, const int32_t* topk_ids,
  *  d_gate     out, float32 [E, H]; NULL: not wanted (not both)
  * Sums are fp32 in a fixed order.  d_gate's products are exact (the fp32
  * d_logits as three bf16 parts); dx, rounded to bf16, leaves out parts below
- * 2^-15 of each product.  T = 0 writes a zero d_gate.  An operand that is
+ * 2^-14 of each product.  T = 0 writes a zero d_gate.  An operand that is
  * not finite makes the rows it meets not finite (an infinity may become a
  * NaN).  Constraints: 0 <= T <= 2^24, H a multiple of 128 and at most 2^20,
  * 1 <= E <= 1024; every pointer but d_logits 16-byte aligned, else

@@ -5,15 +5,21 @@
 //   d_gate[e, h] = sum_t d_logits[t, e] x[t, h]
 //
 // on the matrix cores.  The fp32 operands are split into bf16 planes that add
-// up to them (hi: the value with its low 16 bits cleared, mid and lo: the
-// same for what remains), every product of two planes is exact in fp32 and
+// up to them (hi: the value rounded, mid: the remainder rounded, lo: the
+// rest), every product of two planes is exact in fp32 and
 // v_mfma_f32_16x16x32_bf16 accumulates in fp32:
 //  * d_gate takes all three planes of d_logits against the bf16 x: the sums
 //    are fp32 sums of exact products.
-//  * dx is rounded to bf16 (2^-9 relative), so it takes two planes of
-//    d_logits and of an fp32 gate, without the product of the two mid
-//    planes: what is left out is below 2^-15 of each product.  A bf16 gate
-//    is its own hi plane.
+//  * dx is rounded to bf16 (a half step of 2^-8), so it takes two planes of
+//    d_logits and of an fp32 gate, without the product of the two mid planes.
+//    Left out are mid mid and the two lo parts, each below 2^-16 of the
+//    product: under 2^-14 together.  A bf16 gate is its own hi plane.
+//
+// Bound by the matrix cores: three MFMA products for each fp32 one (two with
+// a bf16 gate).  At 8192 tokens, 7168 columns and 256 experts each of the two
+// products runs in 67 us (kernel alone), 1.35 PFLOP/s of bf16, the rate that
+// a large library product sustains on the card (1.38); the planes take 11 us
+// and the addition of d_gate's 4 splits 7.
 //
 // A first launch writes the planes in the order the MFMA operands read them:
 // fragments of 16 rows x 32 K values, 1 KiB each, lane l of a wave holding
@@ -57,14 +63,16 @@ __device__ __forceinline__ uint32_t lds_addr(const void* p) {
   return (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p;
 }
 // Copy of 16 bytes per lane from byte voff + soff of the range to LDS address
-// dst + 16 lane (copy_frag: 64 lanes x 16 contiguous bytes).  Written as assembly (it has no result
-// register) because the compiler puts a wait for every copy that it knows of
-// ahead of LDS reads it cannot tell from the copy's target, which here would
-// be a wait for the whole pipeline in each step; the waits below are the
-// ones that are needed.  The s_nop is the wait state between a write of m0
-// and its use.
+// dst + 16 lane (copy_frag: 64 lanes x 16 contiguous bytes).  Written as
+// assembly (it has no result register) because the compiler puts a wait for
+// every copy that it knows of ahead of LDS reads it cannot tell from the
+// copy's target, which here would be a wait for the whole pipeline in each
+// step; the waits below are the ones that are needed.  s_mov and s_nop 4 give
+// the wait states that the compiler does not see the need of: one between a
+// write of m0 and its use, five between a vector instruction (readfirstlane)
+// that writes a scalar register and a memory instruction that reads it.
 __device__ __forceinline__ void copy16(const i32x4_t& r, uint32_t voff, uint32_t soff, uint32_t dst) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(
                    __builtin_amdgcn_readfirstlane(dst)),
                "v"(voff), "s"(r), "s"(__builtin_amdgcn_readfirstlane(soff))
                : "memory", "m0");
@@ -87,21 +95,20 @@ __device__ __forceinline__ void step_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// v = hi + mid + lo, each a bf16 (the upper 16 bits of an fp32); a value that
-// is not finite is its own hi plane
+// v = hi + mid + lo, each a bf16 (its 16 bits): hi is v rounded to nearest,
+// mid what remains rounded again, and the rest fits a bf16 (24 bits of v, 8 a
+// plane, and the signs).  A value that is not finite is its own hi plane; one
+// that rounds to infinity keeps its upper bits.
 __device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
   const uint32_t u = __float_as_uint(v);
-  const uint32_t h = u & 0xFFFF0000u;
-  const float r = v - __uint_as_float(h);
-  const uint32_t m = __float_as_uint(r) & 0xFFFF0000u;
-  const float l = r - __uint_as_float(m);
-  hi = h >> 16;
-  mid = m >> 16;
-  lo = __float_as_uint(l) >> 16;
-  if ((u & 0x7F800000u) == 0x7F800000u) {
-    hi |= (u & 0x7FFFFFu) ? 0x40u : 0u;
-    mid = lo = 0u;
-  }
+  hi = cvt_bf16x2(v, 0.f) & 0xFFFFu;
+  const bool special = (hi & 0x7F80u) == 0x7F80u;
+  const bool finite = (u & 0x7F800000u) != 0x7F800000u;
+  if (special && finite) hi = u >> 16;
+  const float r = v - __uint_as_float(hi << 16);
+  mid = cvt_bf16x2(r, 0.f) & 0xFFFFu;
+  lo = cvt_bf16x2(r - __uint_as_float(mid << 16), 0.f) & 0xFFFFu;
+  if (!finite) mid = lo = 0u;
 }
 
 struct GateGradP {
