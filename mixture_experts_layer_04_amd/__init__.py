@@ -1,6 +1,7 @@
 """Single-GPU Mixture-of-Experts layer forward for AMD Instinct MI355X
-(gfx950): HIP kernels behind the C ABI of include/moe.h (libmoe.so) and a
-thin torch binding with the same names."""
+(gfx950), with the norm in front of it and the router's training side: HIP
+kernels behind the C ABI of include/moe.h (libmoe.so) and a thin torch binding
+with the same names."""
 
 from ._lib import LIB_PATH, MoeError, lib  # noqa: F401
 from .ops import (align, align_max_blocks, align_max_padded, balance_loss, debug_error, expert_ffn,  # noqa: F401
