@@ -409,7 +409,10 @@ struct Totals {
 // totals by the workgroup that arrives last, instead of a launch of their own
 // (every arrival is an L2 write-back, 10.3 against 4.8 + 3.5 us at 37
 // sequences of 256 experts), and one workgroup for all of it in small batches
-// (about 4 us a tile: 23 against 14 us at 4096 x 256).
+// (about 4 us a tile: 23 against 14 us at 4096 x 256).  Not kept either: a
+// wave per sequence and tile with its totals by the last of at most 64
+// workgroups (1 to 2 us less below 8192 rows of one sequence, 3 to 4 more at
+// 131072 x 256 in 37 or 150).
 template <int NT>
 __global__ __launch_bounds__(NT) void balance_seq_kernel(BalanceP p) {
   __shared__ SeqSums<NT> sh;

@@ -165,6 +165,7 @@ struct NormP {
   uint16_t* y;  // optional
   uint8_t* q;   // QF != 0
   void* s;
+  int first;  // row of the launch's first workgroup
   int T, H;
   float eps, inv_h;
   int w_fp32;
@@ -213,7 +214,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormP p) {
   const int lanes = p.waves * kWave;  // threads per row
   const int sub = threadIdx.x / lanes, tid = threadIdx.x - sub * lanes;
   const int rows = blockDim.x / lanes;
-  const size_t row = (size_t)blockIdx.x * rows + sub;
+  const size_t row = (size_t)p.first + (size_t)blockIdx.x * rows + sub;
   const bool live = row < (size_t)p.T;
   const bool moved = p.H % kVec != 0;
   Span sp[NV];
@@ -540,15 +541,19 @@ moe_status launch_norm(const void* x, const void* residual, int residual_is_fp32
   // kernel reads them: stored with the non-temporal hint (8192 x 4096 with MX
   // codes 58.8 -> 54.9 us, 8192 x 7168 with an fp32 residual 142 -> 139)
   p.once = (uint64_t)T * H * (2 + (!residual ? 0 : residual_is_fp32 ? 4 : 2)) > (64ull << 20);
-  const dim3 grid((unsigned)ceil_div(T, rows));
-  if ((uint64_t)grid.x * rows * p.waves * kWave > 0xFFFFFFFFull) return MOE_E_UNSUPPORTED;  // HIP's limit of a grid
   const int threads = rows * p.waves * kWave, rt = !residual ? 0 : residual_is_fp32 ? 2 : 1;
-  switch (nv) {
-    case 1: launch_norm_q<1>(p, qformat, rt, grid, threads, stream); break;
-    case 2: launch_norm_q<2>(p, qformat, rt, grid, threads, stream); break;
-    default: launch_norm_q<4>(p, qformat, rt, grid, threads, stream); break;
+  // a grid holds fewer than 2^32 threads: more rows go by several launches
+  const int most = (int)((1u << 31) / threads) * rows;
+  for (int64_t first = 0; first < T; first += most) {
+    p.first = (int)first;
+    const dim3 grid((unsigned)ceil_div(T - first < most ? T - p.first : most, rows));
+    switch (nv) {
+      case 1: launch_norm_q<1>(p, qformat, rt, grid, threads, stream); break;
+      case 2: launch_norm_q<2>(p, qformat, rt, grid, threads, stream); break;
+      default: launch_norm_q<4>(p, qformat, rt, grid, threads, stream); break;
+    }
+    MOE_CHECK_LAUNCH();
   }
-  MOE_CHECK_LAUNCH();
   return MOE_OK;
 }
 

@@ -33,6 +33,23 @@ def test_norm_past_four_gib():
     assert torch.equal(dx[rows], want)
 
 
+def test_norm_of_more_rows_than_one_grid_holds():
+    import mixture_experts_layer_04_amd as moe
+    T, H = (1 << 22) + 3, 8192  # 1024 threads a row; x of 69 GB
+    x = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    rows = torch.tensor([0, 1, (1 << 21) - 1, 1 << 21, (1 << 21) + 1, (1 << 22) - 1, 1 << 22, T - 1], device="cuda")
+    few = torch.randn(len(rows), H, device="cuda").bfloat16()
+    x[rows] = few
+    w = torch.rand(H, device="cuda") + 0.5
+    say("norm", T, H)
+    y, _ = moe.rms_norm(x, w, y=x)
+    want, _ = moe.rms_norm(few, w)
+    torch.cuda.synchronize()
+    assert torch.equal(y[rows], want)
+    del x, y
+    torch.cuda.empty_cache()
+
+
 def test_gate_grad_past_four_gib():
     import mixture_experts_layer_04_amd as moe
     T, H, E = 320000, 7168, 24
