@@ -55,11 +55,19 @@ __device__ __forceinline__ float group_max(float v) {
   return LANES == 16 ? row_max16(v) : wave_max_u(v);
 }
 
-// 4 logits from expert e on; -inf (a score of zero) past the last expert
+typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
+
+// 4 logits from expert e on; -inf (a score of zero) past the last expert.
+// ONCE: with the hint that nobody reads them again soon.
+template <bool ONCE>
 __device__ __forceinline__ void load4(const float* row, int e, int E, float* l) {
   if (e + 4 <= E) {
+    const f32x4_any_t* at = reinterpret_cast<const f32x4_any_t*>(row + e);
     f32x4_t v;
-    __builtin_memcpy(&v, row + e, 16);
+    if constexpr (ONCE)
+      v = __builtin_nontemporal_load(at);
+    else
+      v = *at;
 #pragma unroll
     for (int j = 0; j < 4; ++j) l[j] = v[j];
   } else {
@@ -171,7 +179,7 @@ struct BalanceP {
 // ahead, the mask two).
 // ALL: one workgroup for a small batch of one sequence, which writes the
 // results itself (one launch instead of three).
-template <int LANES, int NV, int SC, int NT, bool ALL>
+template <int LANES, int NV, int SC, int NT, bool ALL, bool ONCE>
 __global__ __launch_bounds__(NT) void balance_kernel(BalanceP p) {
   constexpr int V = 4 * NV, GROUPS = NT / LANES, WAVES = NT / kWave;
   extern __shared__ float lds[];  // [WAVES][Ep] column sums per wave, then [Ep] counts
@@ -200,7 +208,7 @@ __global__ __launch_bounds__(NT) void balance_kernel(BalanceP p) {
       if (!on) return;
       if (j < p.k) slot = p.ids[(size_t)t * p.ks + j];
 #pragma unroll
-      for (int v = 0; v < NV; ++v) load4(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, to + 4 * v);
+      for (int v = 0; v < NV; ++v) load4<ONCE>(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, to + 4 * v);
     };
     bool on = live(lo + g), next = live(lo + g + GROUPS);
     load(lo + g, on, l, id);
@@ -533,7 +541,7 @@ __global__ __launch_bounds__(256) void route_grad_kernel(RouteGradP p) {
       w = p.d_weights[(size_t)t * p.ks + j];
     }
 #pragma unroll
-    for (int v = 0; v < NV; ++v) load4(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, to + 4 * v);
+    for (int v = 0; v < NV; ++v) load4<false>(p.logits + (size_t)t * p.E, (v * LANES + j) * 4, p.E, to + 4 * v);
   };
   load(a + g, l, id, dw, on);
   for (int t = a + g; t < b; t += GROUPS) {
@@ -734,11 +742,20 @@ template <int LANES, int NV, int SC>
 void balance_launch_sc(const BalanceP& p, bool one, hipStream_t s) {
   if constexpr (LANES == 16 && NV <= 4) {
     if (one) {
-      balance_kernel<LANES, NV, SC, 1024, true><<<1, 1024, (size_t)17 * p.Ep * 4, s>>>(p);
+      balance_kernel<LANES, NV, SC, 1024, true, false><<<1, 1024, (size_t)17 * p.Ep * 4, s>>>(p);
       return;
     }
   }
-  balance_kernel<LANES, NV, SC, 256, false><<<p.chunks, 256, (size_t)5 * p.Ep * 4, s>>>(p);
+  // Logits of more than 64 MiB are not in the caches any more, nor is there
+  // room for them beside what is: read with the non-temporal hint (us without
+  // / with it, the whole call: 131072 x 256 39.2 / 36.0, 262144 x 128 37.2 /
+  // 34.0; below, where they may be there still, 65536 x 256 22.3 / 23.4,
+  // 131072 x 64 17.2 / 18.5)
+  const size_t lds = (size_t)5 * p.Ep * 4;
+  if ((uint64_t)p.T * p.E * 4 > (64ull << 20))
+    balance_kernel<LANES, NV, SC, 256, false, true><<<p.chunks, 256, lds, s>>>(p);
+  else
+    balance_kernel<LANES, NV, SC, 256, false, false><<<p.chunks, 256, lds, s>>>(p);
 }
 template <int LANES, int NV>
 void balance_launch(const BalanceP& p, bool one, int scoring, hipStream_t s) {
