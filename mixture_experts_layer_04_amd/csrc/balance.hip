@@ -16,15 +16,15 @@
 //   the others: d = sc' ((gb - sum p gb) / sum(sc) + gw)
 //   both:       d += d_z 2/N lse softmax(l)
 //
-// A token's E logits sit in the registers of 16 neighbouring lanes (64 above
-// 320 experts), so the row sums are four DPP steps and a wave holds four
+// A token's E logits sit in the registers of 16 neighbouring lanes (32 or 64
+// for many experts), so the row sums are four DPP steps and a wave holds four
 // tokens.  The column sums of the loss are accumulated per lane over the
 // tokens of a run, then added across lanes, waves and runs in a fixed order;
 // only integer counts use atomics, so every result is the same in every run.
 //
 // Both read their logits once.  Measured: the loss of 131072 x 256 sigmoid
-// scores in 37 sequences 38.3 us, 31 of them the pass over the 134 MB of
-// logits (4.3 TB/s), the gradient of 65536 x 128 softmax scores 15.2 us (4.7
+// scores in 37 sequences 35.8 us, 28 of them the pass over the 134 MB of
+// logits (4.8 TB/s), the gradient of 65536 x 128 softmax scores 15.2 us (4.7
 // TB/s, as much held by its 84 vector instructions a token as by memory).
 
 #include <cmath>
@@ -46,13 +46,31 @@ __device__ __forceinline__ float row_sum16(float v) {
   v = v + dpp_f32<0x141>(v);
   return v + dpp_f32<0x140>(v);
 }
+// the two rows of 16 lanes that make a group of 32: every lane gets the value
+// of its even row and of its odd one
+struct RowPair {
+  float even, odd;
+};
+__device__ __forceinline__ RowPair row_pair(float v) {
+  const int u = __builtin_bit_cast(int, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return RowPair{__builtin_bit_cast(float, (int)r[0]), __builtin_bit_cast(float, (int)r[1])};
+}
 template <int LANES>
 __device__ __forceinline__ float group_sum(float v) {
-  return LANES == 16 ? row_sum16(v) : wave_sum_u(v);
+  if (LANES == 64) return wave_sum_u(v);
+  v = row_sum16(v);
+  if (LANES == 16) return v;
+  const RowPair r = row_pair(v);
+  return r.even + r.odd;
 }
 template <int LANES>
 __device__ __forceinline__ float group_max(float v) {
-  return LANES == 16 ? row_max16(v) : wave_max_u(v);
+  if (LANES == 64) return wave_max_u(v);
+  v = row_max16(v);
+  if (LANES == 16) return v;
+  const RowPair r = row_pair(v);
+  return fmaxf(r.even, r.odd);
 }
 
 typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
@@ -263,16 +281,12 @@ __global__ __launch_bounds__(NT) void balance_kernel(BalanceP p) {
       on = next;
       next = after;
     }
-    if (LANES == 16) {  // the wave's four tokens
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        acc[i] += __shfl_xor(acc[i], 16, kWave);
-        acc[i] += __shfl_xor(acc[i], 32, kWave);
-      }
-      z += __shfl_xor(z, 16, kWave);
-      z += __shfl_xor(z, 32, kWave);
-      n += __shfl_xor(n, 16, kWave);
-      n += __shfl_xor(n, 32, kWave);
+    for (int off = LANES; off < kWave; off *= 2) {  // the wave's tokens
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += __shfl_xor(acc[i], off, kWave);
+      z += __shfl_xor(z, off, kWave);
+      n += __shfl_xor(n, off, kWave);
     }
     if ((threadIdx.x & 63) < LANES) {
 #pragma unroll
@@ -478,10 +492,10 @@ struct RouteGradP {
   float scale;
 };
 
-// Value of lane i of the caller's group (i uniform).
+// Value of lane i < 16 of the caller's group, for its first 16 lanes.
 template <int LANES, int I>
 __device__ __forceinline__ int group_bcast(int v) {
-  if (LANES == 16) return __builtin_amdgcn_update_dpp(v, v, 0x150 + I, 0xF, 0xF, false);  // row_newbcast
+  if (LANES < 64) return __builtin_amdgcn_update_dpp(v, v, 0x150 + I, 0xF, 0xF, false);  // row_newbcast
   return __builtin_amdgcn_readlane(v, I);
 }
 // sum over the slots i < k that hold this lane's id, of their values, in order
@@ -781,20 +795,28 @@ void route_grad_launch(RouteGradP p, int scoring, hipStream_t s) {
   }
 }
 
-// 16 lanes per token up to 320 experts (20 logits a lane), else 64: above,
-// the gradient's rows would take more registers than two waves per SIMD have.
-#define MOE_BY_EXPERTS(FN, E, ...)             \
-  do {                                         \
-    switch (ceil_div(E, 64)) {                 \
-      case 1: FN<16, 1>(__VA_ARGS__); break;   \
-      case 2: FN<16, 2>(__VA_ARGS__); break;   \
-      case 3: FN<16, 3>(__VA_ARGS__); break;   \
-      case 4: FN<16, 4>(__VA_ARGS__); break;   \
-      case 5: FN<16, 5>(__VA_ARGS__); break;   \
-      case 6: case 7: case 8: FN<64, 2>(__VA_ARGS__); break;              \
-      case 9: case 10: case 11: case 12: FN<64, 3>(__VA_ARGS__); break;   \
-      default: FN<64, 4>(__VA_ARGS__); break;  \
-    }                                          \
+// 16 lanes per token up to 320 experts, 32 above, and MANY above 640: 32 for
+// the loss, 64 for the gradient, which has more per logit in registers.
+// Measured with 16 / 32 / 64 lanes (us, sigmoid): the loss of 65536 tokens and 320
+// experts 28.9 / 35.1 / -, of 448 34.8 / 37.8 / 49.3, of 384 31.7 / 33.0 /
+// 48.6, of 512 34.6 / 33.3 / 42.0 (softmax), of 32768 and 640 - / 29.0 / 36.0,
+// of 1024 - / 37.2 / 39.0; the gradient of 65536 and 128 15.8 / 19.4 / -, of
+// 384 52 / 43 / 58, of 512 78 / 55 / 55, of 16384 and 640 - / 18.1 / 22.2, of
+// 768 - / 23.8 / 23.5, of 32768 and 1024 - / 79 / 53.
+#define MOE_BY_EXPERTS(FN, MANY, E, ...)                                  \
+  do {                                                                    \
+    switch (ceil_div(E, 64)) {                                            \
+      case 1: FN<16, 1>(__VA_ARGS__); break;                              \
+      case 2: FN<16, 2>(__VA_ARGS__); break;                              \
+      case 3: FN<16, 3>(__VA_ARGS__); break;                              \
+      case 4: FN<16, 4>(__VA_ARGS__); break;                              \
+      case 5: FN<16, 5>(__VA_ARGS__); break;                              \
+      case 6: FN<32, 3>(__VA_ARGS__); break;                              \
+      case 7: case 8: FN<32, 4>(__VA_ARGS__); break;                      \
+      case 9: case 10: FN<32, 5>(__VA_ARGS__); break;                     \
+      case 11: case 12: FN<MANY, 192 / MANY>(__VA_ARGS__); break;         \
+      default: FN<MANY, 256 / MANY>(__VA_ARGS__); break;                  \
+    }                                                                     \
   } while (0)
 
 }  // namespace
@@ -849,7 +871,7 @@ extern "C" moe_status moe_balance_loss(const float* logits, const int32_t* topk_
     p.chunks = 1;
   }
   if (T > 0 || one) {
-    MOE_BY_EXPERTS(balance_launch, E, p, one, scoring, stream);
+    MOE_BY_EXPERTS(balance_launch, 32, E, p, one, scoring, stream);
     MOE_CHECK_LAUNCH();
   }
   if (one) return MOE_OK;
@@ -894,7 +916,7 @@ extern "C" moe_status moe_route_grad(const float* logits, const int32_t* topk_id
   p.S = n_seq;
   p.renorm = renormalize != 0;
   p.scale = routed_scale;
-  MOE_BY_EXPERTS(route_grad_launch, E, p, scoring, stream);
+  MOE_BY_EXPERTS(route_grad_launch, 64, E, p, scoring, stream);
   MOE_CHECK_LAUNCH();
   return MOE_OK;
 }

@@ -106,6 +106,38 @@ def test_balance_and_gradient(T, E, k, scoring):
                 assert np.all(f64(d)[seq < 0] == 0)
 
 
+@pytest.mark.parametrize("E", [321, 400, 449, 577, 640, 641, 768, 897, 1023])
+@pytest.mark.parametrize("scoring", SCORINGS)
+def test_many_experts(E, scoring):
+    """Above 320 experts a token's logits lie in 32 or 64 lanes: all 16 slots,
+    ids that repeat in the first and the last of them, foreign ones, and
+    rows of a wave that take no part beside ones that do."""
+    import mixture_experts_layer_04_amd as moe
+    T, k = 77, 16
+    lg, ids = make(T, E, k)
+    ids[0, :] = E - 1
+    ids[1, 15] = ids[1, 0]
+    ids[2, ::2] = 0
+    ids[3, 7] = E
+    ids[4, :] = -1
+    mask = (np.arange(T) % 3 != 1).astype(np.uint8)
+    off = [2, 40, 40, T - 3]
+    offd, maskd = to_dev(off, mask)
+    got = moe.balance_loss(lg, ids, scoring, offd, maskd)
+    ref = ob.balance_loss(f64(lg), ids.cpu().numpy(), scoring, off, mask)
+    seq, _ = ob.members(T, off, mask)
+    check_loss(got, ref, lg, seq)
+    dw = torch.randn(T, k, generator=torch.Generator().manual_seed(E)).cuda()
+    dw[::5] = 0
+    dl = torch.tensor([20.0, 3.0], device="cuda")
+    for renorm in (True, False):
+        d = moe.route_grad(lg, ids, scoring, renorm, 2.5, dw, dl, got[1], got[3], offd, maskd)
+        torch.cuda.synchronize()
+        want, mag = ob.route_grad(f64(lg), ids.cpu().numpy(), scoring, renorm, 2.5, f64(dw), f64(dl), ref["counts"],
+                                  off, mask)
+        assert np.all(np.abs(f64(d) - want) <= mag * 2.0 ** -15 + 1e-35)
+
+
 def test_shared_slot_foreign_and_repeated_ids():
     import mixture_experts_layer_04_amd as moe
     T, E, k = 90, 64, 4
