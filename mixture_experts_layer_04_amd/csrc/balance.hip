@@ -40,39 +40,6 @@ constexpr int kMaxSeqs = 1 << 20;
 constexpr float kTiny = 1e-20f;  // the guard of the router's own renormalisation
 constexpr float kNegInf = -__builtin_huge_valf();
 
-__device__ __forceinline__ float row_sum16(float v) {
-  v = v + dpp_f32<0xB1>(v);
-  v = v + dpp_f32<0x4E>(v);
-  v = v + dpp_f32<0x141>(v);
-  return v + dpp_f32<0x140>(v);
-}
-// the two rows of 16 lanes that make a group of 32: every lane gets the value
-// of its even row and of its odd one
-struct RowPair {
-  float even, odd;
-};
-__device__ __forceinline__ RowPair row_pair(float v) {
-  const int u = __builtin_bit_cast(int, v);
-  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-  return RowPair{__builtin_bit_cast(float, (int)r[0]), __builtin_bit_cast(float, (int)r[1])};
-}
-template <int LANES>
-__device__ __forceinline__ float group_sum(float v) {
-  if (LANES == 64) return wave_sum_u(v);
-  v = row_sum16(v);
-  if (LANES == 16) return v;
-  const RowPair r = row_pair(v);
-  return r.even + r.odd;
-}
-template <int LANES>
-__device__ __forceinline__ float group_max(float v) {
-  if (LANES == 64) return wave_max_u(v);
-  v = row_max16(v);
-  if (LANES == 16) return v;
-  const RowPair r = row_pair(v);
-  return fmaxf(r.even, r.odd);
-}
-
 typedef f32x4_t f32x4_any_t __attribute__((aligned(4)));
 
 // 4 logits from expert e on; -inf (a score of zero) past the last expert.

@@ -100,6 +100,47 @@ __device__ __forceinline__ float wave_sum_u(float v) {
   return (readlane_f32(v, 0) + readlane_f32(v, 16)) + (readlane_f32(v, 32) + readlane_f32(v, 48));
 }
 
+// every lane gets the sum of its 16-lane row
+__device__ __forceinline__ float row_sum16(float v) {
+  v = v + dpp_f32<0xB1>(v);
+  v = v + dpp_f32<0x4E>(v);
+  v = v + dpp_f32<0x141>(v);
+  return v + dpp_f32<0x140>(v);
+}
+// of two neighbouring rows of 16 lanes, every lane gets the value of the even
+// row and of the odd one
+struct RowPair {
+  float even, odd;
+};
+__device__ __forceinline__ RowPair row_pair(float v) {
+  const int u = __builtin_bit_cast(int, v);
+  const auto r = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+  return RowPair{__builtin_bit_cast(float, (int)r[0]), __builtin_bit_cast(float, (int)r[1])};
+}
+// the same for groups of LANES (8, 16, 32 or 64) neighbouring lanes
+template <int LANES>
+__device__ __forceinline__ float group_sum(float v) {
+  if (LANES == 8) {
+    v = v + dpp_f32<0xB1>(v);
+    v = v + dpp_f32<0x4E>(v);
+    return v + dpp_f32<0x141>(v);
+  }
+  if (LANES == 64) return wave_sum_u(v);
+  v = row_sum16(v);
+  if (LANES == 16) return v;
+  const RowPair r = row_pair(v);
+  return r.even + r.odd;
+}
+// LANES 16, 32 or 64
+template <int LANES>
+__device__ __forceinline__ float group_max(float v) {
+  if (LANES == 64) return wave_max_u(v);
+  v = row_max16(v);
+  if (LANES == 16) return v;
+  const RowPair r = row_pair(v);
+  return fmaxf(r.even, r.odd);
+}
+
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
 // Last-workgroup elections: before the barrier that precedes one thread's

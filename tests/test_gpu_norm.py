@@ -224,6 +224,50 @@ def test_norm_grad(T, H, ht, w, with_dh):
     assert torch.equal(dx3, dx) and torch.equal(dw3, dw)  # in place, and the same sums every time
 
 
+NARROW = [(1, 3), (77, 5), (1003, 7), (64, 8), (513, 9), (300, 31), (5, 40), (1001, 63), (4097, 64), (33, 65),
+          (515, 127), (9000, 128), (1030, 129), (70, 200), (2, 255), (2053, 256), (129, 257)]
+
+
+@pytest.mark.parametrize("T,H", NARROW)
+@pytest.mark.parametrize("res,w", [(None, FP32), (BF16, BF16), (FP32, BF16)])
+def test_narrow_rows(T, H, res, w):
+    """Rows of up to 256 values share a wave (8, 4 or 2 of them): the norm, in
+    place too, and its gradient, with rows in the last wave that do not
+    exist."""
+    test_norm(T, H, res, w)
+    test_norm_grad(T, H, BF16 if res is None else res, w, res is not None)
+    import mixture_experts_layer_04_amd as moe
+    x, r, wt = make(T, H, res, w)
+    y, h = moe.rms_norm(x, wt, r)
+    y1, h1 = moe.rms_norm(x, wt, r, y=x, h=r)
+    torch.cuda.synchronize()
+    assert torch.equal(y1, y) and (h is None or torch.equal(h1, h))
+
+
+@pytest.mark.parametrize("quant", ["fp8", "mxfp4"])
+@pytest.mark.parametrize("T,H", [(1001, 32), (1001, 64), (259, 96), (1001, 128), (67, 160), (515, 256)])
+def test_narrow_rows_quantised(quant, T, H):
+    import mixture_experts_layer_04_amd as moe
+    if quant == "fp8" and H % 128:
+        with pytest.raises(ValueError):
+            moe.rms_norm(*make(T, H, None, FP32)[::2], quant=quant)
+        return
+    x, r, wt = make(T, H, BF16, FP32)
+    x[T // 2], r[T // 2] = 0, 0
+    y, h, q, s = moe.rms_norm(x, wt, r, 1e-6, quant)
+    torch.cuda.synchronize()
+    _, ry = check_norm(x, r, wt, y, h)
+    check_quant(quant, q, s, ry)
+
+
+@pytest.mark.parametrize("T,H", [(700, 20001), (300, 16385), (3, 32767), (260, 24576)])
+@pytest.mark.parametrize("ht", [BF16, FP32])
+def test_wide_rows(T, H, ht):
+    """Above 16384 values the weight gradient's sums lie in LDS, over several
+    rows of a workgroup; odd widths in place."""
+    test_norm_grad(T, H, ht, FP32 if ht == BF16 else BF16, True)
+
+
 def test_norm_grad_follows_differences_of_the_forward():
     """The step of y along a direction, taken in the fp32 forward, is the
     gradient's inner product with it."""
