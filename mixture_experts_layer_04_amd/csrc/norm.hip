@@ -18,7 +18,7 @@
 // loads and its stores.  All row vectors are 16-byte accesses at the
 // alignment of an element (the hardware takes them at any address), so odd
 // widths keep the wide accesses.  Measured: 8192 x 4096 with a residual and MX
-// codes 58.5 us (5.2 TB/s; a large copy reaches 4.9 here), its gradient at
+// codes 59 us (5.1 TB/s; a large copy reaches 4.9 here), its gradient at
 // 8192 x 7168 with an fp32 residual stream 155 us (5.3 TB/s); 1 x 7168 3.8
 // us, an empty kernel 3.5.
 //
